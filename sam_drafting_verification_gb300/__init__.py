@@ -15,6 +15,10 @@ the C entry points, over torch CUDA tensors:
   spec_verify(target, draft, ...)       -- spec_verify
   spec_verify_tree(target, tok, ...)    -- spec_verify_tree (draft trees)
   spec_uniforms(B, K, seed, step)       -- spec_uniforms
+  KVCache(...), Rope, rope_frequencies  -- the paged key/value cache of the target
+                                           model (include/samspec_kv.h): .reserve,
+                                           .fork, .commit, .truncate, .plan, .append,
+                                           .attend
 
 Device memory (workspaces, inputs, outputs) comes from torch; each call is
 enqueued on torch's current CUDA stream.
@@ -30,7 +34,7 @@ from ._binding import (BF16, F32, ST_BADDRAFT, ST_BADROW, ST_CAPACITY, ST_HASHFU
                        ST_LOOPCAP, ST_OK, ST_TIMEOUT, ST_TOKEN, SamspecError)
 
 __all__ = ["SamBatch", "spec_verify", "spec_verify_tree", "spec_uniforms", "select_drafts",
-           "SamspecError", "library_path"]
+           "KVCache", "KVPlan", "Rope", "rope_frequencies", "SamspecError", "library_path"]
 
 
 def library_path() -> str:
@@ -512,3 +516,6 @@ def spec_uniforms(B: int, K: int, seed: int, step: int, device=None):
     _b.check(_b.lib().spec_uniforms(int(B), int(K), int(seed) & (2**64 - 1), int(step) & (2**64 - 1),
                                     _ptr(u), _stream(dev)), "spec_uniforms")
     return u
+
+
+from .kvcache import KVCache, KVPlan, Rope, rope_frequencies  # noqa: E402,F401

@@ -20,7 +20,10 @@ CHECKS_LIB_PATH = os.path.join(_HERE, "_lib", "libsamspec_checks.so")
 OK, EINVAL, ESIZE, EDTYPE, ECUDA, EALIGN = 0, -1, -2, -3, -4, -5
 (ST_OK, ST_CAPACITY, ST_HASHFULL, ST_TOKEN, ST_LOOPCAP, ST_BADROW, ST_BADDRAFT, ST_TIMEOUT, ST_BADPARAM,
  ST_BOUNDS) = range(10)
-F32, BF16 = 0, 1
+# include/samspec_kv.h
+ST_PAGE, ST_ROW = 10, 11
+F32, BF16, F16 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = [
     "samspec_version", "samspec_strerror",
@@ -32,6 +35,11 @@ EXPORTED = [
     "spec_verify_tree", "spec_sampling_cut", "spec_verify_sampling_workspace_bytes",
     "spec_verify_sampling", "samspec_set_wait_limit_ns",
 ]
+# the entry points of include/samspec_kv.h
+KV_EXPORTED = [
+    "kv_reserve_workspace_bytes", "kv_reserve", "kv_fork", "kv_commit", "kv_truncate",
+    "kv_plan_bytes", "kv_plan", "kv_append", "kv_attend", "kv_set_wait_limit_ns",
+]
 
 
 class SamspecError(RuntimeError):
@@ -41,6 +49,13 @@ class SamspecError(RuntimeError):
 class VerifyDebug(ctypes.Structure):
     _fields_ = [("row_m", ctypes.c_void_p), ("row_z", ctypes.c_void_p), ("p_d", ctypes.c_void_p),
                 ("q_d", ctypes.c_void_p), ("row_arg", ctypes.c_void_p), ("res_mass", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """struct kv_cache"""
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("k", "v", "table", "lens", "held", "refs", "free_bits")] +
+                [(f, ctypes.c_int32) for f in ("dtype", "layers", "n_pages", "page", "kv_heads", "head_dim",
+                                               "seqs", "max_pages")])
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -84,6 +99,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                          P, P, P, P, P, ctypes.POINTER(VerifyDebug),
                                          I32, P, P, P, P, P, SZ, P]),
     }
+    C, I64 = ctypes.POINTER(KvCacheDesc), ctypes.c_int64
+    sig.update({
+        "kv_reserve_workspace_bytes": (SZ, [C, I32]),
+        "kv_reserve": (ctypes.c_int, [C, P, I32, I32, P, P, P, SZ, P]),
+        "kv_fork": (ctypes.c_int, [C, P, P, I32, P, P]),
+        "kv_commit": (ctypes.c_int, [C, P, I32, I32, P, P, P, P]),
+        "kv_truncate": (ctypes.c_int, [C, P, I32, P, P, P]),
+        "kv_plan_bytes": (SZ, [C, I32, I32, I32, I32]),
+        "kv_plan": (ctypes.c_int, [C, P, I32, I32, I32, P, P, P, P, P, SZ, P]),
+        "kv_append": (ctypes.c_int, [C, I32, P, I32, I32, I32, P, I64, P, P, I64, P, I64, P, I32, I32, F, P]),
+        "kv_attend": (ctypes.c_int, [C, I32, P, SZ, I32, I32, I32, P, I64, F, P, P]),
+        "kv_set_wait_limit_ns": (U64, [U64]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res

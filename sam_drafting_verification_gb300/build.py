@@ -16,7 +16,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsamspec.so")
 CHECKS_LIB = os.path.join(OUT_DIR, "libsamspec_checks.so")
-SOURCES = ["abi.cu", "sam.cu", "sampling.cu", "verify.cu"]
+SOURCES = ["abi.cu", "attend.cu", "cache.cu", "sam.cu", "sampling.cu", "verify.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 
@@ -47,7 +47,7 @@ def _jobs(checks: bool, force: bool, ptxas_info: bool):
     the debug library shares every object but the checked ones."""
     nvcc = nvcc_path()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(ROOT, "include", "samspec.h"))
+    headers += [os.path.join(ROOT, "include", f) for f in ("samspec.h", "samspec_kv.h")]
     objs, cmds = [], []
     for src in SOURCES:
         checked = checks and src in CHECKED_SOURCES

@@ -1,6 +1,7 @@
 // abi.cu -- library-wide entry points of libsamspec.so (version, error text)
 // and the decode step that chains verification and the automata update.
 #include "samspec.h"
+#include "samspec_kv.h"
 
 extern "C" {
 
@@ -23,6 +24,8 @@ const char* samspec_strerror(int code) {
     case SAMSPEC_ST_TIMEOUT: return "sequence: a bounded on-chip wait ran out";
     case SAMSPEC_ST_BADPARAM: return "sequence: temperature not > 0 and finite, or top_p not > 0";
     case SAMSPEC_ST_BOUNDS: return "sequence: an automaton index left its array (debug library)";
+    case SAMSPEC_ST_PAGE: return "sequence: page table or counts do not fit the cache's pool";
+    case SAMSPEC_ST_ROW: return "sequence: row outside the cache, named twice, or not empty";
     default: return "unknown code";
   }
 }

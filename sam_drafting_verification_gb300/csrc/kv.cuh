@@ -1,0 +1,175 @@
+// kv.cuh -- what the paged cache's translation units share: host checks, the
+// device view of a cache, and the layout of a plan.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "samspec.h"
+#include "samspec_kv.h"
+
+namespace samspec {
+
+constexpr int kKvCtas = 152;   // persistent CTAs of kv_attend: one per SM of a GB300
+constexpr int kTileRows = 256; // query rows of a unit of attention work (two MMA tiles)
+constexpr int kKeyBlock = 128; // keys of one step of it
+
+struct KvView {
+  unsigned char* k;
+  unsigned char* v;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* held;
+  int32_t* refs;
+  uint32_t* free_bits;
+  int32_t layers, n_pages, page, log_page, kv_heads, head_dim, seqs, max_pages;
+};
+
+// EINVAL / ESIZE / EDTYPE / EALIGN of a cache descriptor, else OK and its view
+inline int kv_view(const kv_cache* c, KvView* o) {
+  if (!c || !c->k || !c->v || !c->table || !c->lens || !c->held || !c->refs || !c->free_bits)
+    return SAMSPEC_EINVAL;
+  if (c->dtype != SAMSPEC_BF16 && c->dtype != SAMSPEC_F16) return SAMSPEC_EDTYPE;
+  int lg = 4;
+  while (lg < 8 && (1 << lg) != c->page) ++lg;
+  if (lg == 8 || (c->head_dim != 64 && c->head_dim != 128)) return SAMSPEC_ESIZE;
+  if (c->layers < 1 || c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->seqs < 1 ||
+      c->seqs > (1 << 20) || c->max_pages < 1 || c->max_pages > (1 << 20))
+    return SAMSPEC_ESIZE;
+  const int64_t lim = (int64_t)1 << 31;
+  if ((int64_t)c->layers * c->n_pages >= lim || (int64_t)c->n_pages * c->kv_heads * c->page >= lim ||
+      (int64_t)c->max_pages * c->page >= lim)
+    return SAMSPEC_ESIZE;
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) % 16 != 0)
+    return SAMSPEC_EALIGN;
+  *o = {static_cast<unsigned char*>(c->k), static_cast<unsigned char*>(c->v), c->table, c->lens,
+        c->held, c->refs, c->free_bits, c->layers, c->n_pages, c->page, lg, c->kv_heads,
+        c->head_dim, c->seqs, c->max_pages};
+  return SAMSPEC_OK;
+}
+
+// byte offset of (layer, page, head) in a pool: page * head_dim elements of 2
+// bytes follow.  64 bits: a pool passes 4 GB.
+__host__ __device__ inline int64_t kv_offset(const KvView& c, int layer, int page, int head) {
+  return (((int64_t)layer * c.n_pages + page) * c.kv_heads + head) * c.page * c.head_dim * 2;
+}
+
+
+// exclusive prefix sum over a block of 1024 threads; *total the block's sum.
+// `part` is 32 words of shared memory.
+__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFullMask, s, o);
+    if (lane >= o) s += x;
+  }
+  __syncthreads();  // the last call's reads of part
+  if (lane == 31) part[w] = s;
+  __syncthreads();
+  int q = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFullMask, q, o);
+    if (lane >= o) q += x;
+  }
+  const int before = w ? __shfl_sync(kFullMask, q, w - 1) : 0;
+  *total = __shfl_sync(kFullMask, q, 31);
+  return before + s - v;
+}
+
+inline int launched() { return cudaGetLastError() == cudaSuccess ? SAMSPEC_OK : SAMSPEC_ECUDA; }
+
+// ---- plan ------------------------------------------------------------------
+// one sequence of the call
+struct KvSeq {
+  int32_t row;     // its row in the cache
+  int32_t base;    // committed tokens
+  int32_t ntok;    // new tokens (0: a status is set)
+  int32_t leader;  // first sequence of its group
+  int32_t lcp;     // tokens of the pages that it shares with the leader
+  int32_t shared;  // tokens that its group reads once (0: none; at every member)
+  int32_t gsize;   // the group's sequences (at the leader)
+  int32_t pad;
+};
+// a unit of attention work, once for each key head: rows of queries against a
+// range of keys.  Row x is query (x + row0) of sequence i0 on, counted (token,
+// query head within the key head's group), N * rep of them per sequence.
+struct KvTile {
+  int32_t i0, row0, rows;
+  int32_t kbeg, kend;  // tokens
+  int32_t prefix;      // 1: keys that the group shares, every row sees them all
+  int32_t blocks;      // key blocks
+  int32_t cost0;       // blocks of all heads of the tiles before
+};
+enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4, kHdrInts = 16 };
+
+struct PlanLayout {
+  size_t status, hdr, seq, node, suf0, pre0, tile, start, ml, o, bytes;
+  int32_t max_tiles;
+  int64_t store;      // rows of each of the two stores of whole units (grouped plans)
+  int64_t part_rows;  // rows of partial results: two per CTA, then the stores
+};
+
+inline size_t kv_align(size_t x) { return (x + 255) / 256 * 256; }
+
+// 0 bytes where the sizes are outside the limits
+inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_heads, bool grouped) {
+  PlanLayout p = {};
+  if (n < 1 || n > (1 << 20) || N < 1 || N > (1 << 16) || q_heads < 1 || q_heads % c.kv_heads != 0 ||
+      q_heads / c.kv_heads > 64 || (int64_t)n * N * q_heads >= ((int64_t)1 << 30))
+    return p;
+  const int64_t rep = q_heads / c.kv_heads;
+  const int64_t suf = (N * rep + kTileRows - 1) / kTileRows * n;
+  const int64_t pre = grouped ? ((int64_t)n * N * rep + kTileRows - 1) / kTileRows + n : 0;
+  // costs are counted in 32 bits
+  const int64_t blocks = (int64_t)c.max_pages * c.page / kKeyBlock + 2;
+  if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
+  p.max_tiles = (int32_t)(suf + pre);
+  p.store = grouped ? (int64_t)n * N * q_heads : 0;
+  p.part_rows = 2 * kKvCtas * kTileRows + 2 * p.store;
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t o = at; at = kv_align(at + bytes); return o; };
+  p.status = take(4 * (size_t)n);
+  p.hdr = take(4 * kHdrInts);
+  p.seq = take(sizeof(KvSeq) * n);
+  p.node = take(N <= 32 ? 8 * (size_t)n * N : 0);
+  p.suf0 = take(4 * (size_t)n);
+  p.pre0 = take(4 * (size_t)n);
+  p.tile = take(sizeof(KvTile) * (size_t)p.max_tiles);
+  p.start = take(16 * (kKvCtas + 1));
+  p.ml = take(8 * (size_t)p.part_rows);
+  p.o = take(4 * (size_t)p.part_rows * c.head_dim);
+  p.bytes = at;
+  return p;
+}
+
+struct PlanView {
+  int32_t* status;
+  int32_t* hdr;
+  KvSeq* seq;
+  int2* node;      // depth, visible nodes (trees)
+  int32_t* suf0;   // first tile of a sequence's own keys
+  int32_t* pre0;   // first tile of a group's shared keys (at the leader)
+  KvTile* tile;
+  int4* start;     // where each CTA's share begins: tile, head, block, its blocks
+  float2* ml;      // partial results: running maximum (base 2) and sum ...
+  float* o;        // ... and the sums of p v
+  int32_t max_tiles;
+  int64_t store;
+};
+inline PlanView plan_view(void* d_plan, const PlanLayout& p) {
+  unsigned char* b = static_cast<unsigned char*>(d_plan);
+  return {reinterpret_cast<int32_t*>(b + p.status), reinterpret_cast<int32_t*>(b + p.hdr),
+          reinterpret_cast<KvSeq*>(b + p.seq),      reinterpret_cast<int2*>(b + p.node),
+          reinterpret_cast<int32_t*>(b + p.suf0),   reinterpret_cast<int32_t*>(b + p.pre0),
+          reinterpret_cast<KvTile*>(b + p.tile),    reinterpret_cast<int4*>(b + p.start),
+          reinterpret_cast<float2*>(b + p.ml),      reinterpret_cast<float*>(b + p.o),
+          p.max_tiles,                              p.store};
+}
+
+}  // namespace samspec

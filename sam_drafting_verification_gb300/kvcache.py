@@ -1,0 +1,328 @@
+"""The paged key/value cache of the target model and the attention of a
+verification pass (include/samspec_kv.h), over torch CUDA tensors.
+
+A decode step of a model with a cache, between drafting and verification:
+
+    cache.reserve(rows, n_tok)                       # slots for the new tokens
+    plan = cache.plan(N, q_heads, rows=rows, n_tok=n_tok)      # or tree=(first_child, next_sibling)
+    for each layer:
+        q = cache.append(layer, plan, q, k, v, rope) # rotate, write keys and values
+        o = cache.attend(layer, plan, q)             # [n, N, q_heads, head_dim]
+    ... logits, spec_verify / spec_verify_tree ...
+    cache.commit(rows, accept_len, path)             # keep what was accepted
+
+A sequence's new tokens are its last emitted token (not in the cache yet) and
+the K drafts, so N = K + 1; a draft tree's node 0 is that token.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import sys
+
+import torch
+
+from . import _binding as _b
+from . import _cuda_device, _ptr, _req
+
+_pkg = sys.modules[__package__]
+_DTYPES = {torch.bfloat16: _b.BF16, torch.float16: _b.F16}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Radians per position of each of the rot / 2 pairs (fp64, on the host), and
+    the factor that queries and keys are scaled by.  scaling:
+      "none"    base^(-2j / rot)
+      "linear"  positions divided by `factor`
+      "ntk"     the base stretched to base * factor^(rot / (rot - 2)): the
+                lowest frequency divided by factor, the highest kept
+      "yarn"    YaRN (Peng et al. 2023): pairs that turn more than beta_fast
+                times over original_len positions kept, those that turn less
+                than beta_slow times divided by factor, a linear ramp over the
+                pairs between; queries and keys scaled by 0.1 ln(factor) + 1
+    """
+    rot = int(rot)
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling in ("none", "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError(f"unknown scaling {scaling!r}")
+
+    def pair_of(turns):   # the pair that turns so many times over original_len positions
+        return rot * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rot - 1)
+    ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+    return f / factor * ramp + f * (1 - ramp), (0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0)
+
+
+class Rope:
+    """Rotary positions: `inv_freq` fp64 CUDA tensor [rot / 2] (radians per
+    position), layout "half" (pairs (j, j + rot / 2)) or "interleaved" (pairs
+    (2j, 2j + 1)) of the first rot elements of a head, scaled by mscale."""
+
+    def __init__(self, inv_freq, layout: str = "half", mscale: float = 1.0):
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        self.inv_freq = _req(inv_freq, torch.float64, "inv_freq")
+        if inv_freq.dim() != 1 or inv_freq.numel() < 1:
+            raise ValueError("inv_freq must be [rot / 2]")
+        self.rot = 2 * inv_freq.numel()
+        self.layout = _b.ROPE_HALF if layout == "half" else _b.ROPE_INTERLEAVED
+        self.mscale = float(mscale)
+        if not math.isfinite(self.mscale):
+            raise ValueError("mscale must be finite")
+
+
+class KVPlan:
+    """The plan of one pass (KVCache.plan): `status` int32 [n], one word per
+    sequence (0: takes part), and the device memory that kv_append and
+    kv_attend read and work in."""
+
+    def __init__(self, n, N, q_heads, grouped, buf):
+        self.n, self.N, self.q_heads, self.grouped, self.buf = n, N, q_heads, grouped, buf
+        self.bytes = buf.numel()
+        self.ptr = ctypes.c_void_p(buf.data_ptr())
+
+    @property
+    def status(self):
+        return self.buf[:4 * self.n].view(torch.int32)
+
+
+class KVCache:
+    """A paged cache for `seqs` sequences: pools k, v [layers, pages, kv_heads,
+    page, head_dim] (bfloat16 or float16), a page table, committed lengths,
+    pages held, references and free pages.  The tensors are the caller's to
+    read; only the calls below change them."""
+
+    def __init__(self, layers: int, pages: int, page: int, kv_heads: int, head_dim: int, seqs: int,
+                 max_pages: int, dtype=torch.bfloat16, device=None):
+        dev = _cuda_device(device)
+        i32 = lambda *s, fill=0: torch.full(s, fill, dtype=torch.int32, device=dev)  # noqa: E731
+        if dtype not in _DTYPES:
+            raise TypeError("the cache's dtype must be bfloat16 or float16")
+        if min(layers, pages, page, kv_heads, head_dim, seqs, max_pages) < 1:
+            raise ValueError("sizes must be positive")
+        free = i32((pages + 31) // 32, fill=-1)
+        if pages % 32:
+            free[-1] = (1 << pages % 32) - 1
+        self._set(torch.empty((layers, pages, kv_heads, page, head_dim), dtype=dtype, device=dev),
+                  torch.empty((layers, pages, kv_heads, page, head_dim), dtype=dtype, device=dev),
+                  i32(seqs, max_pages, fill=-1), i32(seqs), i32(seqs), i32(pages), free)
+
+    @classmethod
+    def wrap(cls, k, v, table, lens, held, refs, free):
+        """A cache over tensors that the caller holds: k, v [layers, pages,
+        kv_heads, page, head_dim], table int32 [seqs, max_pages], lens and held
+        int32 [seqs], refs int32 [pages], free int32 [ceil(pages / 32)] (a bit
+        for each page, set where refs is 0)."""
+        self = cls.__new__(cls)
+        self._set(k, v, table, lens, held, refs, free)
+        return self
+
+    def _set(self, k, v, table, lens, held, refs, free):
+        if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES:
+            raise TypeError("k must be a bfloat16 or float16 tensor")
+        if k.dim() != 5:
+            raise ValueError("k must be [layers, pages, kv_heads, page, head_dim]")
+        dev = k.device
+        _req(k, k.dtype, "k")
+        _req(v, k.dtype, "v", k.shape, dev)
+        _req(table, torch.int32, "table", None, dev)
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, max_pages]")
+        seqs, max_pages = table.shape
+        layers, pages, kv_heads, page, head_dim = k.shape
+        _req(lens, torch.int32, "lens", (seqs,), dev)
+        _req(held, torch.int32, "held", (seqs,), dev)
+        _req(refs, torch.int32, "refs", (pages,), dev)
+        _req(free, torch.int32, "free", ((pages + 31) // 32,), dev)
+        self.k, self.v, self.table, self.lens, self.held, self.refs, self.free = k, v, table, lens, held, refs, free
+        self.device, self.dtype = dev, k.dtype
+        self.layers, self.pages, self.kv_heads, self.page, self.head_dim = (int(x) for x in k.shape)
+        self.seqs, self.max_pages = int(seqs), int(max_pages)
+        self.lib = _b.lib()
+        self._desc = _b.KvCacheDesc(*(t.data_ptr() for t in (k, v, table, lens, held, refs, free)),
+                                    _DTYPES[k.dtype], *(int(x) for x in (layers, pages, page, kv_heads, head_dim,
+                                                                         seqs, max_pages)))
+        self._ref = ctypes.byref(self._desc)
+
+    # -- helpers ---------------------------------------------------------------
+    def _call(self, name, *args):
+        """The entry point on the device's current stream, with that device
+        current for the launch."""
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                rc = getattr(self.lib, name)(self._ref, *args, _pkg._stream(self.device))
+        else:
+            rc = getattr(self.lib, name)(self._ref, *args, _pkg._stream(self.device))
+        _b.check(rc, name)
+
+    def _i32(self, t, name, shape):
+        return _req(t, torch.int32, name, shape, self.device)
+
+    def _rows(self, rows, n=None):
+        if rows is None:
+            return self.seqs if n is None else n
+        _req(rows, torch.int32, "rows", None if n is None else (n,), self.device)
+        if rows.dim() != 1:
+            raise ValueError("rows must be [n]")
+        return int(rows.shape[0])
+
+    def _status(self, n, out):
+        if out is None:
+            return torch.empty(n, dtype=torch.int32, device=self.device)
+        return self._i32(out, "out", (n,))
+
+    # -- pages -----------------------------------------------------------------
+    def reserve(self, rows, n_tok, out=None):
+        """Room for n_tok more tokens (int32 [n], or one number) behind the
+        committed ones of sequences `rows` (int32 [n], or None for all).  Returns
+        the status words int32 [n]: ST_CAPACITY where pages ran out."""
+        if isinstance(n_tok, torch.Tensor):
+            n = self._rows(rows, int(n_tok.shape[0]) if rows is None and n_tok.dim() == 1 else None)
+            self._i32(n_tok, "n_tok", (n,))
+            most = min(self.max_pages * self.page, 1 << 30)
+        else:
+            n, most, n_tok = self._rows(rows), int(n_tok), None
+        st = self._status(n, out)
+        ws = torch.empty(max(1, int(self.lib.kv_reserve_workspace_bytes(self._ref, n))), dtype=torch.uint8,
+                         device=self.device)
+        self._call("kv_reserve", _ptr(rows), n, most, _ptr(n_tok), _ptr(st), _ptr(ws), ws.numel())
+        return st
+
+    def fork(self, src, dst, out=None):
+        """Sequences dst (int32 [n], empty) become copies of src (int32 [n]),
+        sharing their pages.  Returns the status words int32 [n]."""
+        n = self._rows(src)
+        self._rows(dst, n)
+        st = self._status(n, out)
+        self._call("kv_fork", _ptr(src), _ptr(dst), n, _ptr(st))
+        return st
+
+    def commit(self, rows, accept_len, path=None, out=None):
+        """Keeps the last emitted token and the accepted drafts of a pass:
+        accept_len int32 [n] (spec_verify, spec_verify_tree; -1 keeps nothing),
+        path int32 [n, N] (spec_verify_tree; None for chains).  Returns the
+        status words int32 [n]."""
+        n = self._rows(rows, int(accept_len.shape[0]) if accept_len.dim() == 1 else None)
+        self._i32(accept_len, "accept_len", (n,))
+        N = 1 << 30
+        if path is not None:
+            _req(path, torch.int32, "path", None, self.device)
+            if path.dim() != 2 or path.shape[0] != n:
+                raise ValueError("path must be [n, N]")
+            N = int(path.shape[1])
+        st = self._status(n, out)
+        self._call("kv_commit", _ptr(rows), n, N, _ptr(accept_len), _ptr(path), _ptr(st))
+        return st
+
+    def truncate(self, rows, new_len=None, out=None):
+        """Cuts sequences to at most new_len tokens (int32 [n]; None: empties
+        them) and gives back the pages behind, reserved ones too."""
+        n = self._rows(rows, None if new_len is None else int(new_len.shape[0]))
+        if new_len is not None:
+            self._i32(new_len, "new_len", (n,))
+        st = self._status(n, out)
+        self._call("kv_truncate", _ptr(rows), n, _ptr(new_len), _ptr(st))
+        return st
+
+    # -- a pass ------------------------------------------------------------------
+    def plan(self, N: int, q_heads: int, rows=None, n_tok=None, tree=None, group=None, out=None):
+        """Plans a pass of up to N new tokens for each of the sequences `rows`
+        (int32 [n], or None for all): n_tok int32 [n] of them, a chain (None: N),
+        or tree=(first_child, next_sibling) int32 [n, N] as for spec_verify_tree.
+        group int32 [n]: consecutive sequences of one number read the pages
+        that they share once.  out: the plan of an earlier call with the same
+        sizes, written again in place."""
+        n = self._rows(rows)
+        N, q_heads = int(N), int(q_heads)
+        if n_tok is not None:
+            self._i32(n_tok, "n_tok", (n,))
+        fc = ns = None
+        if tree is not None:
+            if n_tok is not None:
+                n_tok = None   # every node of a tree takes part
+            fc, ns = tree
+            self._i32(fc, "first_child", (n, N))
+            self._i32(ns, "next_sibling", (n, N))
+        if group is not None:
+            self._i32(group, "group", (n,))
+        if out is None:
+            need = int(self.lib.kv_plan_bytes(self._ref, n, N, q_heads, group is not None))
+            if need == 0:
+                raise _b.SamspecError(f"sizes outside the limits: n={n}, N={N}, q_heads={q_heads}")
+            out = KVPlan(n, N, q_heads, group is not None,
+                         torch.empty(need, dtype=torch.uint8, device=self.device))
+        elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.buf.device != self.device or \
+                (group is not None and not out.grouped):
+            raise ValueError("out: a plan of other sizes")
+        self._call("kv_plan", _ptr(rows), n, N, q_heads, _ptr(n_tok), _ptr(fc), _ptr(ns), _ptr(group), out.ptr,
+                   out.bytes)
+        return out
+
+    def _tokens(self, t, name, plan, heads):
+        """t [n, N, heads, head_dim] of the cache's dtype, checked; its token
+        stride in elements.  A view into a wider projection output will do."""
+        if not isinstance(t, torch.Tensor) or not _pkg._is_cuda(t):
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if tuple(t.shape) != (plan.n, plan.N, heads, self.head_dim):
+            raise ValueError(f"{name} must have shape {(plan.n, plan.N, heads, self.head_dim)}, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        s = t.stride()
+        step = s[1] if plan.N > 1 else s[0] if plan.n > 1 else heads * self.head_dim
+        if s[3] != 1 or (heads > 1 and s[2] != self.head_dim) or (plan.n > 1 and s[0] != plan.N * step) \
+                or step < heads * self.head_dim:
+            raise ValueError(f"{name}: tokens must follow one another at one stride, heads and elements without gaps")
+        return step
+
+    def append(self, layer: int, plan: KVPlan, q, k, v, rope: Rope | None = None, out=None):
+        """Writes the new tokens' keys and values k, v [n, N, kv_heads, head_dim]
+        into their slots of `layer`, keys turned to their positions, and returns
+        the turned queries (q [n, N, q_heads, head_dim]; out may be q itself
+        where that is contiguous; None: keys and values only)."""
+        qs = 0
+        if q is not None:
+            qs = self._tokens(q, "q", plan, plan.q_heads)
+            if out is None:
+                out = torch.empty((plan.n, plan.N, plan.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            else:
+                _req(out, self.dtype, "out", q.shape, self.device)
+        else:
+            out = None
+        ks, vs = self._tokens(k, "k", plan, self.kv_heads), self._tokens(v, "v", plan, self.kv_heads)
+        rot, layout, mscale, freq = 0, 0, 1.0, None
+        if rope is not None:
+            rot, layout, mscale, freq = rope.rot, rope.layout, rope.mscale, rope.inv_freq
+            if rot > self.head_dim:
+                raise ValueError("rope: more pairs than the head has")
+            if freq.device != self.device:
+                raise ValueError(f"rope must be on {self.device}, got {freq.device}")
+        self._call("kv_append", int(layer), plan.ptr, plan.n, plan.N, plan.q_heads, _ptr(q), qs, _ptr(out), _ptr(k),
+                   ks, _ptr(v), vs, _ptr(freq), rot, layout, mscale)
+        return out
+
+    def attend(self, layer: int, plan: KVPlan, q, scale: float | None = None, out=None):
+        """softmax(scale q k^T) v of each new token over what it sees (scale:
+        1 / sqrt(head_dim) unless given).  Returns [n, N, q_heads, head_dim];
+        tokens that take no part get zeros."""
+        qs = self._tokens(q, "q", plan, plan.q_heads)
+        if out is None:
+            out = torch.empty((plan.n, plan.N, plan.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+        else:
+            _req(out, self.dtype, "out", q.shape, self.device)
+        self._call("kv_attend", int(layer), plan.ptr, plan.bytes, plan.n, plan.N, plan.q_heads, _ptr(q), qs,
+                   self.head_dim ** -0.5 if scale is None else float(scale), _ptr(out))
+        return out
