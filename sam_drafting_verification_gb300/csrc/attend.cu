@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cmath>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -268,50 +269,729 @@ struct AttendParams {
   int layer, n, N, q_heads, rep;
   const unsigned char* q;
   int64_t q_stride;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;  // scale * log2(e), positive
   unsigned char* out;
+  uint64_t wait_ns;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x) { return (float)x; }
+// Tensor memory and matrix instructions (tcgen05), as inline PTX.
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// arrives on `bar` once every matrix product this thread has issued is done
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// D (tensor memory) = A B (+ D): A and B in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the same with A in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes, one lane a thread
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// true for all where any thread says so
+__device__ __forceinline__ bool named_any(int id, int threads, bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
 
-// One warp a query row, keys one after the other.
 template <typename T>
-__global__ void __launch_bounds__(256) attend_rows_kernel(AttendParams P) {
+struct Type16;
+template <>
+struct Type16<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1, kExponent = 0x7f80;
+  // probabilities relative to a maximum that may lie this many powers of two back
+  static constexpr float kLazy = 8.f, kOffset = 0.f;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
+};
+template <>
+struct Type16<__half> {
+  static constexpr uint32_t kFormat = 0, kExponent = 0x7c00;
+  // fp16 probabilities are held times 2^8: 2^-32 of the largest is still
+  // represented, and 2^15 (a maximum 7 behind) still below its limit
+  static constexpr float kLazy = 7.f, kOffset = 8.f;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 x = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffff)); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+};
+
+// Shared memory of the attention kernel, from a 1024-byte boundary: two tiles
+// of 128 queries, a ring of 128-key tiles (keys and values in turn), control.
+// Every tile is D / 64 slabs of 128 rows of 128 bytes in the 128-byte swizzle
+// (16-byte piece c of row r lies at piece c ^ (r % 8)), which TMA writes and
+// the matrix instructions read.
+template <int D>
+struct Ring {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 11;
+  static constexpr int kCtl = (2 + kStages) * kTile;
+  static constexpr int kBytes = kCtl + 1024 + 1024;  // control, alignment
+};
+struct Ctl {
+  uint64_t full[11], empty[11], s_full[2], p_full[2], o_done, q_full, drain;
+  uint32_t tmem;
+  int32_t abort, bad;
+};
+
+constexpr uint64_t kDescSwizzle128 = (1ull << 46) | (2ull << 61);
+// matrix descriptor of a tile: strides in bytes between slabs (keys across,
+// for the values) and between groups of 8 rows
+__device__ __forceinline__ uint64_t tile_desc(const void* p, uint32_t slab) {
+  return kDescSwizzle128 | (uint64_t)((smem_u32(p) & 0x3ffff) >> 4) | ((uint64_t)(slab >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32);
+}
+
+// A bounded wait: false once the CTA gives up.  The first thread whose wait
+// exceeds the limit raises the flag for all.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, uint64_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (vload(&ctl->abort)) return false;
+    if (global_ns() - t0 > limit) {
+      vstore(&ctl->abort, 1);
+      return false;
+    }
+  }
+  return true;
+}
+// the same without the flag, for what is in flight when a CTA has given up
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity) && global_ns() - t0 < 2000000000ull) {
+  }
+}
+
+// A CTA's share of the work: blocks of consecutive units (tile, key head).
+struct Walk {
+  int tile, head, blk, left;
+  KvTile t;
+  int nb;  // blocks of the segment in hand
+  __device__ __forceinline__ Walk(const AttendParams& P) {
+    const int4 a = P.plan.start[blockIdx.x];
+    left = P.plan.start[blockIdx.x + 1].w - a.w;
+    tile = a.x;
+    head = a.y;
+    blk = a.z;
+    load(P);
+  }
+  __device__ __forceinline__ void load(const AttendParams& P) {
+    if (left > 0) {
+      const int4* s = reinterpret_cast<const int4*>(P.plan.tile + tile);
+      int4* d = reinterpret_cast<int4*>(&t);
+      d[0] = s[0];
+      d[1] = s[1];
+      nb = min(left, t.blocks - blk);
+    }
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool whole() const { return nb == t.blocks; }
+  __device__ __forceinline__ void next(const AttendParams& P) {
+    left -= nb;
+    blk = 0;
+    if (++head == P.c.kv_heads) {
+      head = 0;
+      ++tile;
+    }
+    load(P);
+  }
+};
+
+// One persistent CTA an SM, 12 warps.  Warp 8 loads pages by TMA, warp 9
+// issues matrix products, two warpgroups do the softmax, a thread a row.
+//
+// A step is one block of 128 keys against 128 query rows: S = Q K^T (both in
+// shared memory, S in tensor memory), P = exp2(S - m) rounded to 16 bits over
+// S's columns, O += P V.  Two streams of steps run at once, each with its own
+// S, running maximum, sum and O, so that the matrix unit works on one while
+// the other's softmax runs: a unit of more than 128 rows has a stream for each
+// half of its rows (both use a block of keys and values while it is in shared
+// memory), a smaller one gives even and odd blocks to the two and adds them up
+// at the end.  O is rescaled only when the maximum has moved by 2^kLazy.
+//
+// Few rows (a decode step has N * rep of 128) waste the matrix unit but not
+// memory time: at 128 keys * D * 4 bytes a step HBM takes about 2800 clocks an
+// SM, the two products 1024, a warp's softmax about 800.
+template <typename T, int D>
+__global__ void __launch_bounds__(384, 1)
+    attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  using R = Ring<D>;
+  using H = Type16<T>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + R::kCtl);
+  unsigned char* ring = smem + 2 * R::kTile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const KvView& c = P.c;
-  const int lane = threadIdx.x & 31, D = c.head_dim;
+  if ((int)blockIdx.x >= P.plan.hdr[kHdrCtas]) return;  // before anything is set up
+  if (warp == 9) tmem_alloc(&ctl->tmem, 512);
+  if (tid == 0) {
+    for (int s = 0; s < R::kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&ctl->s_full[w], 1);
+      mbar_init(&ctl->p_full[w], 128);
+    }
+    mbar_init(&ctl->o_done, 1);
+    mbar_init(&ctl->q_full, 256);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    ctl->bad = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const uint32_t tS = tmem, tO = tmem + 256;  // streams 128 columns apart
+  const bool tree = P.plan.hdr[kHdrTree] != 0;
+  Walk wk(P);
+
+  // registers: 384 * 168 at launch = 256 * 224 + 128 * 56
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 8) {
+    // ---- pages to the ring ----
+    int kt = 0;  // tiles requested
+    bool ok = true;
+    for (; ok && wk.more(); wk.next(P)) {
+      const KvSeq sq = P.plan.seq[wk.t.i0];
+      const int32_t* table = c.table + (int64_t)sq.row * c.max_pages;
+      const int per = kKeyBlock >> c.log_page;  // pages of a block
+      constexpr int kSlabs = D / 64;
+      const int x = lane / kSlabs, slab = lane % kSlabs;
+      int key0 = wk.t.kbeg + wk.blk * kKeyBlock;
+      int page = 0;
+      auto fetch = [&](int k0) {
+        const int p = (k0 >> c.log_page) + x;
+        return x < per && p << c.log_page < wk.t.kend ? table[p] : -1;
+      };
+      page = fetch(key0);
+      for (int b = 0; ok && b < wk.nb; ++b) {
+        const int ahead = b + 1 < wk.nb ? fetch(key0 + kKeyBlock) : -1;
+        const int pages = __popc(__ballot_sync(kFullMask, page >= 0 && slab == 0));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++kt) {
+          const int st = kt % R::kStages;
+          ok = ok && wait_for(&ctl->empty[st], ((kt / R::kStages) & 1) ^ 1, ctl, P.wait_ns);
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], (uint32_t)pages * c.page * D * 2);
+          __syncwarp();
+          if (page >= 0)
+            tma_load3(ring + st * R::kTile + slab * (128 * 128) + x * c.page * 128, kv ? &map_v : &map_k, slab * 64,
+                      wk.head * c.page, P.layer * c.n_pages + page, &ctl->full[st]);
+        }
+        page = ahead;
+        key0 += kKeyBlock;
+      }
+    }
+    // given up: what was requested has to land before the CTA may end
+    if (!ok)
+      for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
+        drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
+  } else if (warp == 9) {
+    // ---- matrix products ----
+    if (lane == 0) {
+      const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
+      const uint32_t id_s = id | ((128 >> 3) << 17), id_o = id | ((D >> 3) << 17) | (1u << 16);
+      int kt = 0, seg = 0, pc[2] = {0, 0};
+      bool ok = true;
+      for (; ok && wk.more(); wk.next(P), ++seg) {
+        const bool rows2 = wk.t.rows > 128;
+        const int items = rows2 ? 2 * wk.nb : wk.nb;
+        ok = wait_for(&ctl->q_full, seg & 1, ctl, P.wait_ns);
+        for (int x = 0; ok && x <= items; ++x) {
+          if (x < items) {
+            const int w = x & 1, t = kt + 2 * (rows2 ? x >> 1 : x), st = t % R::kStages;
+            if (!rows2 || w == 0) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = tile_desc(smem + (rows2 ? w : 0) * R::kTile, 16384);
+            const uint64_t kd = tile_desc(ring + st * R::kTile, 16384);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = (k / 4) * (16384 >> 4) + (k % 4) * 2;  // 16 elements along a row
+              mma_ss(tS + 128 * w, qd + at, kd + at, id_s, k > 0);
+            }
+            mma_commit(&ctl->s_full[w]);
+            if (!rows2 || w == 1) mma_commit(&ctl->empty[st]);
+          }
+          if (x > 0) {
+            const int y = x - 1, w = y & 1, blk = rows2 ? y >> 1 : y, t = kt + 2 * blk + 1, st = t % R::kStages;
+            ok = wait_for(&ctl->p_full[w], pc[w] & 1, ctl, P.wait_ns);
+            ++pc[w];
+            if (ok && (!rows2 || w == 0)) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = tile_desc(ring + st * R::kTile, 16384);
+            const bool first = rows2 ? blk == 0 : y < 2;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows
+              mma_ts(tO + 128 * w, tS + 128 * w + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+            if (!rows2 || w == 1) mma_commit(&ctl->empty[st]);
+          }
+        }
+        if (ok) mma_commit(&ctl->o_done);
+        kt += 2 * wk.nb;
+      }
+      if (!ok) {
+        mma_commit(&ctl->drain);
+        drain_wait(&ctl->drain, 0);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---- softmax
+    // A thread that gives up keeps taking part in every barrier and arrival
+    // of its segment, without work, so that no other waits for it. ----
+    const int w = warp >> 2;              // stream
+    const int row = tid & 127;            // its row, and its lane of tensor memory
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes;
+    const float sc = P.scale_log2;
+    const int spr = P.N * P.rep;
+    int kb = 0, seg = 0, sp = 0;  // blocks before this segment; steps of this stream
+    bool ok = true;
+    for (; ok && wk.more(); wk.next(P), ++seg) {
+      const KvTile& t = wk.t;
+      const bool rows2 = t.rows > 128;
+      // queries of this unit: 16 bytes a thread, a row by D / 8 threads
+      {
+        constexpr int kPer = D / 8;
+        const int r0 = rows2 ? 128 * w : 64 * w, cnt = rows2 ? 128 : 64;
+        unsigned char* dst = smem + (rows2 ? w : 0) * R::kTile;
+        for (int x = row; x < cnt * kPer; x += 128) {
+          const int r = r0 + x / kPer, pc = x % kPer;
+          if (r < t.rows) {
+            const int rr = t.row0 + r, i = t.i0 + rr / spr, in = rr % spr;
+            const int node = in / P.rep, j = in % P.rep;
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                P.q + (((int64_t)i * P.N + node) * P.q_stride + (int64_t)(wk.head * P.rep + j) * D) * 2 + pc * 16);
+            const int rt = r & 127;
+            *reinterpret_cast<uint4*>(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4)) = v;
+          }
+        }
+        if (tid == 0) ctl->bad = 0;
+        fence_async_smem();
+        tc_fence_before();  // the last segment's reads of tensor memory
+        mbar_arrive(&ctl->q_full);
+      }
+      // this thread's row: what it sees of the new tokens
+      const int r = rows2 ? 128 * w + row : row;
+      const int rr = t.row0 + r;
+      const int i = t.i0 + rr / spr, node = rr % spr / P.rep, hq = wk.head * P.rep + rr % P.rep;
+      const bool in = r < t.rows;
+      int base = t.kend, lim = t.kend, ntok = 0;
+      uint32_t see = 0;
+      if (in) {
+        ntok = P.plan.seq[i].ntok;
+        if (!t.prefix) {
+          base = P.plan.seq[i].base;
+          if (tree) {
+            see = (uint32_t)P.plan.node[(int64_t)i * P.N + node].y;
+            lim = base;
+          } else {
+            lim = min(t.kend, base + node + 1);
+          }
+        }
+      }
+      const bool live = in && node < ntok;
+      const int ctx = t.prefix ? t.kend : P.plan.seq[t.i0].base;  // keys before it need no mask
+      const bool busy = (rows2 ? 128 * w : 0) + 32 * (warp & 3) < t.rows;
+      float m = -INFINITY, l = 0.f;  // m in units of raw scores
+      const int items = rows2 ? 2 * wk.nb : wk.nb;
+      for (int x = w; x < items; x += 2, ++sp) {
+        const int b = rows2 ? x >> 1 : x;
+        const int k0 = t.kbeg + (wk.blk + b) * kKeyBlock;
+        const bool edge = k0 + kKeyBlock > ctx;
+        if (ok) ok = wait_for(&ctl->s_full[w], sp & 1, ctl, P.wait_ns);
+        ok = __all_sync(kFullMask, ok);
+        tc_fence_after();
+        if (ok && busy) {
+          uint32_t s[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(mS + 32 * q, s + 32 * q);
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int ks = k0 + 32 * q;
+              // bits of the 32 keys from ks on: those before lim, and a tree's
+              uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
+              if (see) {
+                const int d = base - ks;
+                bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1)) s[32 * q + e] = 0xff800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(s[q]);
+#pragma unroll
+          for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float f = 1.f;
+          if (m == -INFINITY) {
+            m = top;  // nothing of weight has been added up so far
+          } else if ((top - m) * sc > H::kLazy) {
+            f = ex2_approx((m - top) * sc);
+            m = top;
+          }
+          if (x >= 2 && __any_sync(kFullMask, live && f != 1.f)) {
+            l *= f;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(mO + 32 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(mO + 32 * q, o);
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : H::kOffset - m * sc;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float a = ex2_approx(fmaf(__uint_as_float(s[64 * q + 2 * e]), sc, off));
+              const float d = ex2_approx(fmaf(__uint_as_float(s[64 * q + 2 * e + 1]), sc, off));
+              sum[e & 3] += a + d;
+              p[e] = H::pack(a, d);
+            }
+            tmem_st32(mS + 32 * q, p);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        if (edge) {
+          // values that no query of the unit sees become zeros, and so do
+          // infinities and NaN of new tokens, which only some see (0 * NaN
+          // would reach the others): those that do see them add them at the end
+          const int t_v = 2 * (kb + b) + 1, st = t_v % R::kStages;
+          if (ok) ok = wait_for(&ctl->full[st], (t_v / R::kStages) & 1, ctl, P.wait_ns);
+          if (ok && (!rows2 || w == 0)) {
+            constexpr int kPer = D / 8;
+            const int lo = max(ctx - k0, 0), hi = min(t.kend - k0, kKeyBlock);
+            unsigned char* v = ring + st * R::kTile;
+            bool found = false;
+            for (int e = row; e < (kKeyBlock - lo) * kPer; e += 128) {
+              const int r1 = lo + e / kPer, pc = e % kPer;
+              uint4* at = reinterpret_cast<uint4*>(v + (pc >> 3) * 16384 + r1 * 128 + (((pc & 7) ^ (r1 & 7)) << 4));
+              if (r1 >= hi) {
+                *at = uint4{0, 0, 0, 0};
+              } else {
+                uint4 u = *at;
+                uint32_t* a = reinterpret_cast<uint32_t*>(&u);
+                bool hit = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t lo16 = (a[k] & H::kExponent) == H::kExponent ? 0xffffu : 0u;
+                  const uint32_t hi16 = ((a[k] >> 16) & H::kExponent) == H::kExponent ? 0xffff0000u : 0u;
+                  hit |= (lo16 | hi16) != 0;
+                  a[k] &= ~(lo16 | hi16);
+                }
+                if (hit) *at = u;
+                found |= hit;
+              }
+            }
+            if (found) ctl->bad = 1;
+            fence_async_smem();
+          }
+          if (rows2) named_sync(3, 256);
+          else named_sync(1 + w, 128);
+        }
+        tc_fence_before();
+        mbar_arrive(&ctl->p_full[w]);
+      }
+      kb += wk.nb;
+      if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
+      ok = !named_any(4, 256, !ok);  // all threads of both streams decide alike
+      if (!ok) break;
+      tc_fence_after();
+      const bool both = !rows2 && items > 1;
+      float2* ml = reinterpret_cast<float2*>(smem);  // the queries' place: they have been used
+      if (!rows2) {
+        ml[128 * w + row] = {m, l};
+        named_sync(4, 256);
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (!rows2) {
+        if (both) {
+          const float2 a = ml[row], z = ml[128 + row];
+          m = fmaxf(a.x, z.x);
+          const float mm = m == -INFINITY ? 0.f : m;
+          f0 = ex2_approx((a.x - mm) * sc);
+          f1 = ex2_approx((z.x - mm) * sc);
+          l = a.y * f0 + z.y * f1;
+        } else {
+          m = ml[row].x;  // stream 0 had the only block
+          l = ml[row].y;
+        }
+      }
+      const int d0 = rows2 ? 0 : w * (D / 2), d1 = rows2 ? D : d0 + D / 2;
+      const bool direct = wk.whole() && P.plan.seq[t.i0].shared == 0;
+      float* part = nullptr;
+      int64_t slot = 0;
+      if (!direct) {
+        if (wk.whole()) {
+          slot = 2 * kKvCtas * kTileRows + (t.prefix ? P.plan.store : 0) +
+                 (((int64_t)i * P.N + node) * P.q_heads + hq);
+        } else {
+          // the first segment of a CTA's share, or its last
+          slot = (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + r;
+        }
+        part = P.plan.o + slot * D;
+      }
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      if (busy) {
+        const uint32_t a0 = tO + lanes + (rows2 ? 128 * w : 0);
+        for (int d = d0; d < d1; d += 32) {
+          uint32_t u[32];
+          float o[32];
+          tmem_ld32(a0 + d, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+          if (both) {
+            tmem_ld32(a0 + 128 + d, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(u[e]) * f1;
+          }
+          if (live) {
+          if (ctl->bad && !t.prefix) {
+            // infinities and NaN that this row does see
+            for (int key = max(base, t.kbeg + wk.blk * kKeyBlock);
+                 key < min(t.kend, t.kbeg + (wk.blk + wk.nb) * kKeyBlock); ++key) {
+              if (!(key < lim || (see && key - base < 32 && ((see >> (key - base)) & 1)))) continue;
+              const int pg = c.table[(int64_t)P.plan.seq[i].row * c.max_pages + (key >> c.log_page)];
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                  c.v + kv_offset(c, P.layer, pg, wk.head) + ((int64_t)(key & (c.page - 1)) * D + d) * 2);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t z = v[e];
+                if ((z & H::kExponent) == H::kExponent) o[2 * e] += H::lo(z);
+                if (((z >> 16) & H::kExponent) == H::kExponent) o[2 * e + 1] += H::hi(z);
+              }
+            }
+          }
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                P.out + ((((int64_t)i * P.N + node) * P.q_heads + hq) * D + d) * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = {H::pack(o[8 * e] * inv, o[8 * e + 1] * inv), H::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                        H::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv), H::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv)};
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part + d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = {o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]};
+          }
+          }
+          __syncwarp();
+        }
+        if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+      }
+      // both streams are done with the exchange and the flag before new
+      // queries replace them
+      named_sync(4, 256);
+    }
+    if (!ok) {
+      // the sequences of this and the following units have no result
+      for (; wk.more(); wk.next(P)) {
+        const int last = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / spr;
+        for (int k = wk.t.i0 + tid; k <= last; k += 256) P.plan.status[k] = SAMSPEC_ST_TIMEOUT;
+      }
+      if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_free(tmem, 512);
+}
+
+// Rows of units that were cut among CTAs, or that have a shared part: their
+// partial results joined.  One warp a row; others' rows are passed over, those
+// of no token become zeros.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(AttendParams P) {
+  using H = Type16<T>;
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= (int64_t)P.n * P.N * P.q_heads) return;
-  const int h = (int)(r % P.q_heads);
+  const int hq = (int)(r % P.q_heads);
   const int64_t tok = r / P.q_heads;
   const int i = (int)(tok / P.N), node = (int)(tok % P.N);
   const KvSeq s = P.plan.seq[i];
-  T* out = reinterpret_cast<T*>(P.out) + r * D;
+  uint32_t* out = reinterpret_cast<uint32_t*>(P.out + r * D * 2) + lane * (kPer / 2);
   if (node >= s.ntok) {
-    for (int d = lane; d < D; d += 32) out[d] = (T)0.f;
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) out[e] = 0;
     return;
   }
-  const T* q = reinterpret_cast<const T*>(P.q) + tok * P.q_stride + h * D;
-  const uint32_t see = P.plan.hdr[kHdrTree] ? (uint32_t)P.plan.node[tok].y : 0;
-  const bool tree = P.plan.hdr[kHdrTree] != 0;
-  float qv[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
-  for (int x = 0; x < D / 32; ++x) qv[x] = to_f(q[lane + 32 * x]);
-  const int end = s.base + (tree ? s.ntok : node + 1);
-  for (int key = 0; key < end; ++key) {
-    if (tree && key >= s.base && !((see >> (key - s.base)) & 1)) continue;
-    const int page = c.table[(int64_t)s.row * c.max_pages + (key >> c.log_page)];
-    const int64_t at = kv_offset(c, P.layer, page, h / P.rep) + (int64_t)(key & (c.page - 1)) * D * 2;
-    const T* k = reinterpret_cast<const T*>(c.k + at);
-    const T* v = reinterpret_cast<const T*>(c.v + at);
-    float a = 0;
-    for (int x = 0; x < D / 32; ++x) a += qv[x] * to_f(k[lane + 32 * x]);
-    a = warp_sum(a) * P.scale_log2;
-    const float mn = fmaxf(m, a), f = mn == -INFINITY ? 1.f : exp2f(m - mn), p = exp2f(a - (mn == -INFINITY ? 0.f : mn));
-    for (int x = 0; x < D / 32; ++x) o[x] = o[x] * f + p * to_f(v[lane + 32 * x]);
-    l = l * f + p;
+  const int h = hq / P.rep, x = node * P.rep + hq % P.rep;
+  const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
+  float m = -INFINITY, l = 0.f, o[kPer] = {};
+  auto add = [&](int64_t slot) {
+    const float2 z = P.plan.ml[slot];
+    const float* a = P.plan.o + slot * D + lane * kPer;
+    const float mn = fmaxf(m, z.x), mm = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - mm), g = exp2f(z.x - mm);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = o[e] * f + a[e] * g;
+    l = l * f + z.y * g;
     m = mn;
+  };
+  for (int part = s.shared > 0 ? 0 : 1; part < 2; ++part) {
+    const int at = part ? x : (i - s.leader) * P.N * P.rep + x;
+    const int ti = (part ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + at / kTileRows;
+    const KvTile t = P.plan.tile[ti];
+    const int b0 = t.cost0 + h * t.blocks, b1 = b0 + t.blocks;
+    // the last CTA that begins at or before a block
+    const int c0 = (int)((((int64_t)b0 + 1) * ctas - 1) / cost), c1 = (int)(((int64_t)b1 * ctas - 1) / cost);
+    if (c0 == c1) {
+      if (s.shared == 0) return;  // written where it was computed
+      add(2 * kKvCtas * kTileRows + (part ? 0 : P.plan.store) + r);
+    } else {
+      for (int q = c0; q <= c1; ++q)
+        add((int64_t)(2 * q + (q == c0 && P.plan.start[q].w != b0)) * kTileRows + at % kTileRows);
+    }
   }
-  for (int x = 0; x < D / 32; ++x) out[lane + 32 * x] = (T)(l > 0 || l != l ? o[x] / l : 0.f);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+}
+
+// cuTensorMapEncodeTiled, looked up once: the library links no driver
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> cached{nullptr};
+  void* f = cached.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    cached.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// a pool as [layers * n_pages][kv_heads * page][head_dim], in boxes of one
+// page and head, 64 elements wide
+int pool_map(const KvView& c, int32_t dtype, void* pool, CUtensorMap* map) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return SAMSPEC_ECUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.kv_heads * c.page, (cuuint64_t)c.layers * c.n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, (cuuint64_t)c.kv_heads * c.page * c.head_dim * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)c.page, 1}, one[3] = {1, 1, 1};
+  return enc(map, dtype == SAMSPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, pool,
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SAMSPEC_OK
+             : SAMSPEC_ECUDA;
+}
+
+template <typename T, int D>
+int attend(const AttendParams& P, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  if (cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes) !=
+      cudaSuccess)
+    return SAMSPEC_ECUDA;
+  attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv);
+  const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
+  join_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(P);
+  return launched();
 }
 
 // the layout that plan_bytes bytes were asked for
@@ -369,7 +1049,7 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   AttendParams P;
   const int rc = kv_view(cache, &P.c);
   if (rc != SAMSPEC_OK) return rc;
-  if (!d_plan || !d_q || !d_out || layer < 0 || layer >= P.c.layers || !std::isfinite(scale))
+  if (!d_plan || !d_q || !d_out || layer < 0 || layer >= P.c.layers || !std::isfinite(scale) || !(scale > 0))
     return SAMSPEC_EINVAL;
   PlanLayout l;
   if (!plan_of(P.c, n, N, q_heads, plan_bytes, &l)) return SAMSPEC_ESIZE;
@@ -387,13 +1067,14 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   P.q_stride = q_stride;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.out = static_cast<unsigned char*>(d_out);
-  const int64_t rows = (int64_t)n * N * q_heads;
+  P.wait_ns = g_kv_wait_ns.load();
+  CUtensorMap mk, mv;
+  if (pool_map(P.c, cache->dtype, cache->k, &mk) != SAMSPEC_OK || pool_map(P.c, cache->dtype, cache->v, &mv) != SAMSPEC_OK)
+    return SAMSPEC_ECUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->dtype == SAMSPEC_BF16)
-    attend_rows_kernel<__nv_bfloat16><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(P);
-  else
-    attend_rows_kernel<__half><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(P);
-  return launched();
+    return cache->head_dim == 64 ? attend<__nv_bfloat16, 64>(P, mk, mv, s) : attend<__nv_bfloat16, 128>(P, mk, mv, s);
+  return cache->head_dim == 64 ? attend<__half, 64>(P, mk, mv, s) : attend<__half, 128>(P, mk, mv, s);
 }
 
 uint64_t kv_set_wait_limit_ns(uint64_t ns) {
