@@ -159,6 +159,9 @@ __global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
 // One CTA: what a group reads once, the units of work and their order, and
 // each persistent CTA's equal share of the key blocks.
 constexpr int kMinShared = 128;  // tokens: less is read by each sequence for itself
+// what a unit costs besides its blocks (its queries, the start and end of its
+// two streams), in blocks
+constexpr int kUnitCost = 2;
 
 __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __shared__ int part[32];
@@ -230,12 +233,12 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   for (int t0 = 0; t0 < tiles; t0 += 1024) {
     const int t = t0 + tid;
     int sum;
-    const int at = block_scan(t < tiles ? P.plan.tile[t].blocks * c.kv_heads : 0, part, &sum);
+    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks + kUnitCost) * c.kv_heads : 0, part, &sum);
     if (t < tiles) P.plan.tile[t].cost0 = cost + at;
     cost += sum;
   }
   __syncthreads();
-  const int ctas = min(kKvCtas, cost);
+  const int ctas = min(kKvCtas, cost);  // at most one CTA begins at any cost
   for (int x = tid; x <= ctas; x += 1024) {
     const int b = ctas ? (int)((int64_t)x * cost / ctas) : 0;
     int lo = 0, hi = tiles - 1;  // the last tile that begins at or before b
@@ -244,12 +247,15 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
       if (P.plan.tile[mid].cost0 <= b) lo = mid;
       else hi = mid - 1;
     }
-    int4 s = {0, 0, 0, b};
+    // the cost b lies in: unit (lo, y), at its block z; w counts all blocks before
+    int4 s = {0, 0, 0, cost - kUnitCost * c.kv_heads * tiles};
     if (x < ctas) {
       const KvTile t = P.plan.tile[lo];
+      const int u = t.blocks + kUnitCost;
       s.x = lo;
-      s.y = (b - t.cost0) / t.blocks;
-      s.z = (b - t.cost0) % t.blocks;
+      s.y = (b - t.cost0) / u;
+      s.z = max((b - t.cost0) % u - kUnitCost, 0);
+      s.w = t.cost0 - kUnitCost * c.kv_heads * lo + s.y * t.blocks + s.z;
     }
     P.plan.start[x] = s;
   }
@@ -417,18 +423,22 @@ __device__ __forceinline__ uint64_t tile_desc(const void* p, uint32_t slab) {
 }
 
 // A bounded wait: false once the CTA gives up.  The first thread whose wait
-// exceeds the limit raises the flag for all.
+// exceeds the limit raises the flag for all.  The clock is read only every
+// 256 tries.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, uint64_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t k = limit < 1000000 ? 0 : 1;; ++k) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (k & 255) continue;
     if (vload(&ctl->abort)) return false;
-    if (global_ns() - t0 > limit) {
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit) {
       vstore(&ctl->abort, 1);
       return false;
     }
   }
-  return true;
 }
 // the same without the flag, for what is in flight when a CTA has given up
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
@@ -636,22 +646,32 @@ __global__ void __launch_bounds__(384, 1)
     for (; ok && wk.more(); wk.next(P), ++seg) {
       const KvTile& t = wk.t;
       const bool rows2 = t.rows > 128;
-      // queries of this unit: 16 bytes a thread, a row by D / 8 threads
+      // queries of this unit, 16 bytes a copy: a lane finds its row's address,
+      // the warp's copies are all in flight at once (one after the other they
+      // took 14 us a unit)
       {
-        constexpr int kPer = D / 8;
-        const int r0 = rows2 ? 128 * w : 64 * w, cnt = rows2 ? 128 : 64;
+        constexpr int kPer = D / 8;              // copies of a row
+        constexpr int kRows = 32 / kPer;         // rows of one step of the warp
+        const int cnt = rows2 ? 32 : 16;         // rows of this warp
+        const int r0 = rows2 ? 32 * (warp & 3) : 64 * w + 16 * (warp & 3);
         unsigned char* dst = smem + (rows2 ? w : 0) * R::kTile;
-        for (int x = row; x < cnt * kPer; x += 128) {
-          const int r = r0 + x / kPer, pc = x % kPer;
-          if (r < t.rows) {
-            const int rr = t.row0 + r, i = t.i0 + rr / spr, in = rr % spr;
-            const int node = in / P.rep, j = in % P.rep;
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                P.q + (((int64_t)i * P.N + node) * P.q_stride + (int64_t)(wk.head * P.rep + j) * D) * 2 + pc * 16);
-            const int rt = r & 127;
-            *reinterpret_cast<uint4*>(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4)) = v;
-          }
+        const int lr = (rows2 ? 128 * w : 0) + r0 + lane;
+        int64_t mine = -1;
+        if (lane < cnt && lr < t.rows) {
+          const int rr = t.row0 + lr, i = t.i0 + rr / spr, in = rr % spr;
+          mine = ((int64_t)i * P.N + in / P.rep) * P.q_stride + (int64_t)(wk.head * P.rep + in % P.rep) * D;
         }
+        const int pc = lane % kPer;
+        for (int x = 0; x < cnt; x += kRows) {
+          const int e = x + lane / kPer, rt = r0 + e;
+          const int64_t from = __shfl_sync(kFullMask, mine, e);
+          if (from >= 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4))),
+                         "l"(P.q + from * 2 + pc * 16)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (tid == 0) ctl->bad = 0;
         fence_async_smem();
         tc_fence_before();  // the last segment's reads of tensor memory
@@ -899,56 +919,98 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Rows of units that were cut among CTAs, or that have a shared part: their
-// partial results joined.  One warp a row; others' rows are passed over, those
-// of no token become zeros.
+// partial results joined.  Rows that were written where they were computed are
+// passed over, those of no token become zeros.  A warp takes 8 rows: a lane
+// finds where one row's parts lie, then the warp adds up one row after the
+// other, the loads of up to 4 parts in flight at once.
+constexpr int kJoinRows = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(AttendParams P) {
   using H = Type16<T>;
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= (int64_t)P.n * P.N * P.q_heads) return;
-  const int hq = (int)(r % P.q_heads);
-  const int64_t tok = r / P.q_heads;
-  const int i = (int)(tok / P.N), node = (int)(tok % P.N);
-  const KvSeq s = P.plan.seq[i];
-  uint32_t* out = reinterpret_cast<uint32_t*>(P.out + r * D * 2) + lane * (kPer / 2);
-  if (node >= s.ntok) {
-#pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) out[e] = 0;
-    return;
-  }
-  const int h = hq / P.rep, x = node * P.rep + hq % P.rep;
-  const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
-  float m = -INFINITY, l = 0.f, o[kPer] = {};
-  auto add = [&](int64_t slot) {
-    const float2 z = P.plan.ml[slot];
-    const float* a = P.plan.o + slot * D + lane * kPer;
-    const float mn = fmaxf(m, z.x), mm = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - mm), g = exp2f(z.x - mm);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = o[e] * f + a[e] * g;
-    l = l * f + z.y * g;
-    m = mn;
+  struct alignas(4 * kPer) Vec {
+    float x[kPer];
   };
-  for (int part = s.shared > 0 ? 0 : 1; part < 2; ++part) {
-    const int at = part ? x : (i - s.leader) * P.N * P.rep + x;
-    const int ti = (part ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + at / kTileRows;
-    const KvTile t = P.plan.tile[ti];
-    const int b0 = t.cost0 + h * t.blocks, b1 = b0 + t.blocks;
-    // the last CTA that begins at or before a block
-    const int c0 = (int)((((int64_t)b0 + 1) * ctas - 1) / cost), c1 = (int)(((int64_t)b1 * ctas - 1) / cost);
-    if (c0 == c1) {
-      if (s.shared == 0) return;  // written where it was computed
-      add(2 * kKvCtas * kTileRows + (part ? 0 : P.plan.store) + r);
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
+  const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoinRows;
+  if (r0 >= rows) return;
+  // of lane's row: parts (-1: none to join, 0: zeros), and for the shared and
+  // the own keys where the first part lies and where the others begin
+  int parts = -1, first[2] = {0, 0}, rest[2] = {0, 0}, cnt[2] = {0, 0};
+  const int64_t mine = r0 + lane;
+  if (lane < kJoinRows && mine < rows) {
+    const int hq = (int)(mine % P.q_heads);
+    const int64_t tok = mine / P.q_heads;
+    const int i = (int)(tok / P.N), node = (int)(tok % P.N);
+    const KvSeq s = P.plan.seq[i];
+    if (node >= s.ntok) {
+      parts = 0;
     } else {
-      for (int q = c0; q <= c1; ++q)
-        add((int64_t)(2 * q + (q == c0 && P.plan.start[q].w != b0)) * kTileRows + at % kTileRows);
+      const int h = hq / P.rep, x = node * P.rep + hq % P.rep;
+      const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (p == 0 && s.shared == 0) continue;
+        const int at = p ? x : (i - s.leader) * P.N * P.rep + x;
+        const int ti = (p ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + at / kTileRows;
+        const KvTile t = P.plan.tile[ti];
+        const int b0 = t.cost0 + h * (t.blocks + kUnitCost);  // the unit's costs begin
+        // the CTAs that hold its first and its last block: the last that
+        // begins at or before each
+        const int c0 = (int)((((int64_t)b0 + kUnitCost + 1) * ctas - 1) / cost);
+        const int c1 = (int)((((int64_t)b0 + kUnitCost + t.blocks) * ctas - 1) / cost);
+        cnt[p] = c1 - c0 + 1;
+        if (c0 == c1) {
+          if (s.shared == 0) cnt[p] = 0;
+          first[p] = (int)(2 * kKvCtas * kTileRows + (p ? 0 : P.plan.store) + mine);
+        } else {
+          // the first segment of a CTA's share, or its last
+          const bool begins = (int64_t)c0 * cost / ctas >= b0;
+          first[p] = (2 * c0 + !begins) * kTileRows + at % kTileRows;
+          rest[p] = 2 * (c0 + 1) * kTileRows + at % kTileRows;
+        }
+      }
+      parts = cnt[0] + cnt[1];
+      if (parts == 0) parts = -1;
     }
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  for (uint32_t todo = __ballot_sync(kFullMask, parts >= 0); todo; todo &= todo - 1) {
+    const int w = __ffs(todo) - 1;
+    const int n = __shfl_sync(kFullMask, parts, w), n0 = __shfl_sync(kFullMask, cnt[0], w);
+    const int f0 = __shfl_sync(kFullMask, first[0], w), f1 = __shfl_sync(kFullMask, first[1], w);
+    const int s0 = __shfl_sync(kFullMask, rest[0], w), s1 = __shfl_sync(kFullMask, rest[1], w);
+    float m = -INFINITY, l = 0.f, o[kPer] = {};
+    for (int q = 0; q < n; q += 4) {
+      float2 z[4];
+      Vec a[4];
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+      for (int e = 0; e < 4; ++e) {
+        const int k = q + e;
+        z[e] = {-INFINITY, 0.f};
+        if (k < n) {
+          const int j = k < n0 ? k : k - n0;
+          const int64_t slot = j == 0 ? (k < n0 ? f0 : f1) : (k < n0 ? s0 : s1) + (j - 1) * 2 * kTileRows;
+          z[e] = P.plan.ml[slot];
+          a[e] = *reinterpret_cast<const Vec*>(P.plan.o + slot * D + lane * kPer);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (q + e < n) {
+          const float mn = fmaxf(m, z[e].x), mm = mn == -INFINITY ? 0.f : mn;
+          const float f = exp2f(m - mm), g = exp2f(z[e].x - mm);
+#pragma unroll
+          for (int d = 0; d < kPer; ++d) o[d] = o[d] * f + a[e].x[d] * g;
+          l = l * f + z[e].y * g;
+          m = mn;
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(P.out + (r0 + w) * D * 2) + lane * (kPer / 2);
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+  }
 }
 
 // cuTensorMapEncodeTiled, looked up once: the library links no driver
@@ -990,7 +1052,7 @@ int attend(const AttendParams& P, const CUtensorMap& mk, const CUtensorMap& mv, 
     return SAMSPEC_ECUDA;
   attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  join_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(P);
+  join_kernel<T, D><<<(unsigned)((rows + 8 * kJoinRows - 1) / (8 * kJoinRows)), 256, 0, s>>>(P);
   return launched();
 }
 

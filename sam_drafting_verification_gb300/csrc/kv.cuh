@@ -104,7 +104,7 @@ struct KvTile {
   int32_t kbeg, kend;  // tokens
   int32_t prefix;      // 1: keys that the group shares, every row sees them all
   int32_t blocks;      // key blocks
-  int32_t cost0;       // blocks of all heads of the tiles before
+  int32_t cost0;       // cost of all heads of the tiles before
 };
 enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4, kHdrInts = 16 };
 
@@ -127,7 +127,7 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
   const int64_t suf = (N * rep + kTileRows - 1) / kTileRows * n;
   const int64_t pre = grouped ? ((int64_t)n * N * rep + kTileRows - 1) / kTileRows + n : 0;
   // costs are counted in 32 bits
-  const int64_t blocks = (int64_t)c.max_pages * c.page / kKeyBlock + 2;
+  const int64_t blocks = (int64_t)c.max_pages * c.page / kKeyBlock + 8;
   if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
   p.max_tiles = (int32_t)(suf + pre);
   p.store = grouped ? (int64_t)n * N * q_heads : 0;
