@@ -211,16 +211,22 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
         KvTile t;
         t.i0 = i;
         t.row0 = k * kTileRows;
-        t.prefix = pass == 0;
+        t.base = seq[i].base;
+        t.ntok = seq[i].ntok;
+        t.seq_row = seq[i].row;
         if (pass == 0) {
           t.rows = min(kTileRows, seq[i].gsize * rows - t.row0);
           t.kbeg = 0;
-          t.kend = seq[i].shared;
+          t.kend = t.ctx = seq[i].shared;
+          t.kind = 1;
         } else {
-          t.rows = min(kTileRows, seq[i].ntok * P.rep - t.row0);
+          t.rows = min(kTileRows, t.ntok * P.rep - t.row0);
           t.kbeg = seq[i].shared;
-          // a chain's tile sees no further than its last token
-          t.kend = seq[i].base + (P.first_child ? seq[i].ntok : (t.row0 + t.rows - 1) / P.rep + 1);
+          // a chain's tile sees no further than its last token, and all of it
+          // up to its first; a tree's nodes all see the root
+          t.kend = t.base + (P.first_child ? t.ntok : (t.row0 + t.rows - 1) / P.rep + 1);
+          t.ctx = t.base + (P.first_child ? 1 : t.row0 / P.rep + 1);
+          t.kind = t.kbeg > 0 ? 2 : 0;
         }
         t.blocks = (t.kend - t.kbeg + kKeyBlock - 1) / kKeyBlock;
         t.cost0 = 0;
@@ -291,7 +297,16 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// waits for this thread's loads; the 32 registers cannot be used before it
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // arrives on `bar` once every matrix product this thread has issued is done
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -327,15 +342,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -401,17 +429,24 @@ struct Type16<__half> {
 // Every tile is D / 64 slabs of 128 rows of 128 bytes in the 128-byte swizzle
 // (16-byte piece c of row r lies at piece c ^ (r % 8)), which TMA writes and
 // the matrix instructions read.
+struct Segment {  // what the queries' loader hands on of a segment
+  KvTile t;
+  int32_t head, blk, nb, pad;
+};
+struct Ctl {
+  uint64_t full[11], empty[11], s_full[2], p_full[2], q_full[2], q_empty[2], o_done, o_free, drain;
+  uint32_t tmem;
+  int32_t abort, bad;
+  float2 ml[256];  // running maxima and sums that the streams exchange
+  alignas(16) Segment seg[4];
+};
 template <int D>
 struct Ring {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 11;
   static constexpr int kCtl = (2 + kStages) * kTile;
-  static constexpr int kBytes = kCtl + 1024 + 1024;  // control, alignment
-};
-struct Ctl {
-  uint64_t full[11], empty[11], s_full[2], p_full[2], o_done, q_full, drain;
-  uint32_t tmem;
-  int32_t abort, bad;
+  static constexpr int kBytes = kCtl + (int)((sizeof(Ctl) + 127) / 128 * 128);
+  static_assert(kBytes <= 232448, "227 KB of a CTA");
 };
 
 constexpr uint64_t kDescSwizzle128 = (1ull << 46) | (2ull << 61);
@@ -463,14 +498,12 @@ struct Walk {
   __device__ __forceinline__ void load(const AttendParams& P) {
     if (left > 0) {
       const int4* s = reinterpret_cast<const int4*>(P.plan.tile + tile);
-      int4* d = reinterpret_cast<int4*>(&t);
-      d[0] = s[0];
-      d[1] = s[1];
+      const int4 a = s[0], b = s[1], c = s[2];
+      t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
       nb = min(left, t.blocks - blk);
     }
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ bool whole() const { return nb == t.blocks; }
   __device__ __forceinline__ void next(const AttendParams& P) {
     left -= nb;
     blk = 0;
@@ -482,8 +515,97 @@ struct Walk {
   }
 };
 
+// Two floats in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 bytes a thread: a whole sector
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Values of a block from row `lo` on (the keys that not every query sees):
+// those of no key of the unit (from row `hi` on) become zeros, and so do
+// infinities and NaN, since 0 * NaN would reach the queries that do not see
+// them; those that do add them at the end.  `th` of `threads` threads.
+template <typename T, int D>
+__device__ __forceinline__ void clean_values(unsigned char* v, int lo, int hi, int th, int threads, Ctl* ctl) {
+  using H = Type16<T>;
+  constexpr int kPer = D / 8;
+  bool found = false;
+  for (int e = th; e < (kKeyBlock - lo) * kPer; e += threads) {
+    const int r = lo + e / kPer, pc = e % kPer;
+    uint4* at = reinterpret_cast<uint4*>(v + (pc >> 3) * 16384 + r * 128 + (((pc & 7) ^ (r & 7)) << 4));
+    if (r >= hi) {
+      *at = uint4{0, 0, 0, 0};
+    } else {
+      uint4 u = *at;
+      uint32_t* a = reinterpret_cast<uint32_t*>(&u);
+      bool hit = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo16 = (a[k] & H::kExponent) == H::kExponent ? 0xffffu : 0u;
+        const uint32_t hi16 = ((a[k] >> 16) & H::kExponent) == H::kExponent ? 0xffff0000u : 0u;
+        hit |= (lo16 | hi16) != 0;
+        a[k] &= ~(lo16 | hi16);
+      }
+      if (hit) *at = u;
+      found |= hit;
+    }
+  }
+  if (found) ctl->bad = 1;
+  fence_async_smem();
+}
+
+// Infinities and NaN among the values of keys [from, to) that a row sees,
+// added to its stored result (out: 16 bits, else fp32 sums), columns d0 on.
+template <typename T>
+__device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, int head, int base, int lim, uint32_t see,
+                                         int from, int to, int d0, int cols, unsigned char* out, float* sums) {
+  using H = Type16<T>;
+  const KvView& c = P.c;
+  for (int key = from; key < to; ++key) {
+    if (!(key < lim || (key >= base && key - base < 32 && ((see >> (key - base)) & 1)))) continue;
+    const int pg = c.table[(int64_t)seq_row * c.max_pages + (key >> c.log_page)];
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+        c.v + kv_offset(c, P.layer, pg, head) + ((int64_t)(key & (c.page - 1)) * c.head_dim + d0) * 2);
+    for (int e = 0; e < cols / 2; ++e) {
+      const uint32_t z = v[e];
+      const bool lo = (z & H::kExponent) == H::kExponent, hi = ((z >> 16) & H::kExponent) == H::kExponent;
+      if (!lo && !hi) continue;
+      if (out) {
+        uint32_t* o = reinterpret_cast<uint32_t*>(out) + e;
+        *o = H::pack(H::lo(*o) + (lo ? H::lo(z) : 0.f), H::hi(*o) + (hi ? H::hi(z) : 0.f));
+      } else {
+        if (lo) sums[2 * e] += H::lo(z);
+        if (hi) sums[2 * e + 1] += H::hi(z);
+      }
+    }
+  }
+}
+
 // One persistent CTA an SM, 12 warps.  Warp 8 loads pages by TMA, warp 9
-// issues matrix products, two warpgroups do the softmax, a thread a row.
+// issues matrix products, warps 10 and 11 load queries, two warpgroups do the
+// softmax, a thread a row.
 //
 // A step is one block of 128 keys against 128 query rows: S = Q K^T (both in
 // shared memory, S in tensor memory), P = exp2(S - m) rounded to 16 bits over
@@ -491,25 +613,31 @@ struct Walk {
 // S, running maximum, sum and O, so that the matrix unit works on one while
 // the other's softmax runs: a unit of more than 128 rows has a stream for each
 // half of its rows (both use a block of keys and values while it is in shared
-// memory), a smaller one gives even and odd blocks to the two and adds them up
+// memory), a smaller one gives its blocks to the two in turn and adds them up
 // at the end.  O is rescaled only when the maximum has moved by 2^kLazy.
+// Steps are numbered through all of a CTA's segments, step g in stream g % 2,
+// so the next segment's first scores are computed while this one's last are
+// worked on; only its first product into O waits until O has been read.
 //
 // Few rows (a decode step has N * rep of 128) waste the matrix unit but not
 // memory time: at 128 keys * D * 4 bytes a step HBM takes about 2800 clocks an
-// SM, the two products 1024, a warp's softmax about 800.
+// SM, the two products 1024, a warp's softmax about 1500 with two in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(384, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
   using R = Ring<D>;
   using H = Type16<T>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem[];
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + R::kCtl);
   unsigned char* ring = smem + 2 * R::kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const KvView& c = P.c;
   if ((int)blockIdx.x >= P.plan.hdr[kHdrCtas]) return;  // before anything is set up
+  if (smem_u32(smem) & 1023) {  // the swizzle counts from there; the linker sees to it
+    if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
+    return;
+  }
   if (warp == 9) tmem_alloc(&ctl->tmem, 512);
   if (tid == 0) {
     for (int s = 0; s < R::kStages; ++s) {
@@ -518,10 +646,12 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl->s_full[w], 1);
-      mbar_init(&ctl->p_full[w], 128);
+      mbar_init(&ctl->p_full[w], 4);
+      mbar_init(&ctl->q_full[w], 2);
+      mbar_init(&ctl->q_empty[w], 2);  // its products are done, its segment has been seen
     }
     mbar_init(&ctl->o_done, 1);
-    mbar_init(&ctl->q_full, 256);
+    mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     ctl->bad = 0;
@@ -532,70 +662,90 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   const uint32_t tS = tmem, tO = tmem + 256;  // streams 128 columns apart
-  const bool tree = P.plan.hdr[kHdrTree] != 0;
-  Walk wk(P);
+  const int spr = P.N * P.rep;
 
-  // registers: 384 * 168 at launch = 256 * 224 + 128 * 56
+  // registers: 384 * 168 at launch = 256 * 216 + 128 * 72
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 8) {
-    // ---- pages to the ring ----
-    int kt = 0;  // tiles requested
-    bool ok = true;
-    for (; ok && wk.more(); wk.next(P)) {
-      const KvSeq sq = P.plan.seq[wk.t.i0];
-      const int32_t* table = c.table + (int64_t)sq.row * c.max_pages;
-      const int per = kKeyBlock >> c.log_page;  // pages of a block
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      // ---- pages to the ring ----
+      int kt = 0;  // tiles requested
+      bool ok = true;
       constexpr int kSlabs = D / 64;
       const int x = lane / kSlabs, slab = lane % kSlabs;
-      int key0 = wk.t.kbeg + wk.blk * kKeyBlock;
-      int page = 0;
-      auto fetch = [&](int k0) {
-        const int p = (k0 >> c.log_page) + x;
-        return x < per && p << c.log_page < wk.t.kend ? table[p] : -1;
-      };
-      page = fetch(key0);
-      for (int b = 0; ok && b < wk.nb; ++b) {
-        const int ahead = b + 1 < wk.nb ? fetch(key0 + kKeyBlock) : -1;
-        const int pages = __popc(__ballot_sync(kFullMask, page >= 0 && slab == 0));
+      const int per = kKeyBlock >> c.log_page;  // pages of a block
+      for (Walk wk(P); ok && wk.more(); wk.next(P)) {
+        const int32_t* table = c.table + (int64_t)wk.t.seq_row * c.max_pages;
+        int key0 = wk.t.kbeg + wk.blk * kKeyBlock;
+        auto fetch = [&](int k0) {
+          const int p = (k0 >> c.log_page) + x;
+          return x < per && p << c.log_page < wk.t.kend ? table[p] : -1;
+        };
+        int page = fetch(key0);
+        for (int b = 0; ok && b < wk.nb; ++b) {
+          const int ahead = b + 1 < wk.nb ? fetch(key0 + kKeyBlock) : -1;
+          const int pages = __popc(__ballot_sync(kFullMask, page >= 0 && slab == 0));
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++kt) {
-          const int st = kt % R::kStages;
-          ok = ok && wait_for(&ctl->empty[st], ((kt / R::kStages) & 1) ^ 1, ctl, P.wait_ns);
-          ok = __all_sync(kFullMask, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], (uint32_t)pages * c.page * D * 2);
-          __syncwarp();
-          if (page >= 0)
-            tma_load3(ring + st * R::kTile + slab * (128 * 128) + x * c.page * 128, kv ? &map_v : &map_k, slab * 64,
-                      wk.head * c.page, P.layer * c.n_pages + page, &ctl->full[st]);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = kt % R::kStages;
+            ok = ok && wait_for(&ctl->empty[st], ((kt / R::kStages) & 1) ^ 1, ctl, P.wait_ns);
+            ok = __all_sync(kFullMask, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], (uint32_t)pages * c.page * D * 2);
+            __syncwarp();
+            if (page >= 0)
+              tma_load3(ring + st * R::kTile + slab * (128 * 128) + x * c.page * 128, kv ? &map_v : &map_k, slab * 64,
+                        wk.head * c.page, P.layer * c.n_pages + page, &ctl->full[st]);
+            ++kt;
+          }
+          page = ahead;
+          key0 += kKeyBlock;
         }
-        page = ahead;
-        key0 += kKeyBlock;
       }
-    }
-    // given up: what was requested has to land before the CTA may end
-    if (!ok)
-      for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
-        drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
-  } else if (warp == 9) {
-    // ---- matrix products ----
-    if (lane == 0) {
-      const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
-      const uint32_t id_s = id | ((128 >> 3) << 17), id_o = id | ((D >> 3) << 17) | (1u << 16);
-      int kt = 0, seg = 0, pc[2] = {0, 0};
-      bool ok = true;
-      for (; ok && wk.more(); wk.next(P), ++seg) {
-        const bool rows2 = wk.t.rows > 128;
-        const int items = rows2 ? 2 * wk.nb : wk.nb;
-        ok = wait_for(&ctl->q_full, seg & 1, ctl, P.wait_ns);
-        for (int x = 0; ok && x <= items; ++x) {
-          if (x < items) {
-            const int w = x & 1, t = kt + 2 * (rows2 ? x >> 1 : x), st = t % R::kStages;
-            if (!rows2 || w == 0) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
+      // given up: what was requested has to land before the CTA may end
+      if (!ok)
+        for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
+          drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
+    } else if (warp == 9) {
+      // ---- matrix products ----
+      if (lane == 0) {
+        const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
+        const uint32_t id_s = id | ((128 >> 3) << 17), id_o = id | ((D >> 3) << 17) | (1u << 16);
+        bool ok = true;
+        // the step whose product with V is still to be issued (-1: none): its
+        // ring tile, whether it begins an O, ends a use of the tile, a segment
+        int v_tile = -1, v_seg = 0;
+        bool v_first = false, v_wait = false, v_last = false, v_end = false;
+        int g = 0;  // steps issued
+        auto product = [&] {
+          const int w = (g - 1) & 1, st = v_tile % R::kStages;
+          ok = wait_for(&ctl->p_full[w], ((g - 1) >> 1) & 1, ctl, P.wait_ns);
+          if (ok && v_wait) ok = wait_for(&ctl->full[st], (v_tile / R::kStages) & 1, ctl, P.wait_ns);
+          // the last segment's O has to be read before this one's begins
+          if (ok && v_first && v_seg > 0) ok = wait_for(&ctl->o_free, (v_seg - 1) & 1, ctl, P.wait_ns);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t vd = tile_desc(ring + st * R::kTile, 16384);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows
+            mma_ts(tO + 128 * w, tS + 128 * w + 8 * k, vd + k * (2048 >> 4), id_o, !v_first || k > 0);
+          if (v_last) mma_commit(&ctl->empty[st]);
+          if (v_end) mma_commit(&ctl->o_done);
+          v_tile = -1;
+        };
+        int kt = 0, qt = 0, seg = 0;
+        for (Walk wk(P); ok && wk.more(); wk.next(P), ++seg) {
+          const bool rows2 = wk.t.rows > 128;
+          const int items = rows2 ? 2 * wk.nb : wk.nb;
+          for (int q = 0; ok && q < (rows2 ? 2 : 1); ++q)
+            ok = wait_for(&ctl->q_full[(qt + q) & 1], ((qt + q) >> 1) & 1, ctl, P.wait_ns);
+          for (int x = 0; ok && x < items; ++x, ++g) {
+            const int w = g & 1, half = rows2 ? x & 1 : 0, b = rows2 ? x >> 1 : x;
+            const int t = kt + 2 * b, st = t % R::kStages;
+            if (half == 0) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = tile_desc(smem + (rows2 ? w : 0) * R::kTile, 16384);
+            const uint64_t qd = tile_desc(smem + ((qt + half) & 1) * R::kTile, 16384);
             const uint64_t kd = tile_desc(ring + st * R::kTile, 16384);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -603,119 +753,134 @@ __global__ void __launch_bounds__(384, 1)
               mma_ss(tS + 128 * w, qd + at, kd + at, id_s, k > 0);
             }
             mma_commit(&ctl->s_full[w]);
-            if (!rows2 || w == 1) mma_commit(&ctl->empty[st]);
+            const bool last = !rows2 || half == 1;
+            if (last) mma_commit(&ctl->empty[st]);
+            if (x + 1 >= items - rows2) mma_commit(&ctl->q_empty[(qt + half) & 1]);
+            if (v_tile >= 0) product();
+            v_tile = t + 1;
+            v_seg = seg;
+            v_first = x < 2;
+            v_wait = half == 0;
+            v_last = last;
+            v_end = x == items - 1;
           }
-          if (x > 0) {
-            const int y = x - 1, w = y & 1, blk = rows2 ? y >> 1 : y, t = kt + 2 * blk + 1, st = t % R::kStages;
-            ok = wait_for(&ctl->p_full[w], pc[w] & 1, ctl, P.wait_ns);
-            ++pc[w];
-            if (ok && (!rows2 || w == 0)) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = tile_desc(ring + st * R::kTile, 16384);
-            const bool first = rows2 ? blk == 0 : y < 2;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows
-              mma_ts(tO + 128 * w, tS + 128 * w + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
-            if (!rows2 || w == 1) mma_commit(&ctl->empty[st]);
-          }
+          kt += 2 * wk.nb;
+          qt += rows2 ? 2 : 1;
         }
-        if (ok) mma_commit(&ctl->o_done);
-        kt += 2 * wk.nb;
+        if (ok && v_tile >= 0) product();
+        if (!ok) {
+          mma_commit(&ctl->drain);
+          drain_wait(&ctl->drain, 0);
+        }
       }
-      if (!ok) {
-        mma_commit(&ctl->drain);
-        drain_wait(&ctl->drain, 0);
+      __syncwarp();
+    } else {
+      // ---- queries ----
+      // Two warps, 64 rows of a tile each, one segment ahead of the products.
+      // A lane finds its rows' addresses; all copies are in flight at once.
+      bool ok = true;
+      int qt = 0, seg = 0;
+      for (Walk wk(P); ok && wk.more(); wk.next(P), ++seg) {
+        const bool rows2 = wk.t.rows > 128;
+        for (int half = 0; half < (rows2 ? 2 : 1); ++half, ++qt) {
+          ok = ok && wait_for(&ctl->q_empty[qt & 1], ((qt >> 1) & 1) ^ 1, ctl, P.wait_ns);
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          constexpr int kPer = D / 8;       // copies of a row
+          constexpr int kRows = 32 / kPer;  // rows of one step of the warp
+          unsigned char* dst = smem + (qt & 1) * R::kTile;
+          const int pc = lane % kPer;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int r0 = 64 * (warp - 10) + 32 * z, lr = 128 * half + r0 + lane;
+            int64_t mine = -1;
+            if (lr < wk.t.rows) {
+              const int rr = wk.t.row0 + lr, i = wk.t.i0 + rr / spr, in = rr % spr;
+              mine = ((int64_t)i * P.N + in / P.rep) * P.q_stride + (int64_t)(wk.head * P.rep + in % P.rep) * D;
+            }
+#pragma unroll
+            for (int y = 0; y < 32; y += kRows) {
+              const int e = y + lane / kPer, rt = r0 + e;
+              const int64_t from = __shfl_sync(kFullMask, mine, e);
+              if (from >= 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4))),
+                             "l"(P.q + from * 2 + pc * 16)
+                             : "memory");
+            }
+          }
+          if (warp == 10 && lane == 0 && half == 0)
+            ctl->seg[seg & 3] = {wk.t, wk.head, wk.blk, wk.nb, 0};
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->q_full[qt & 1]);
+        }
       }
     }
-    __syncwarp();
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ---- softmax ----
     // A thread that gives up keeps taking part in every barrier and arrival
-    // of its segment, without work, so that no other waits for it. ----
-    const int w = warp >> 2;              // stream
-    const int row = tid & 127;            // its row, and its lane of tensor memory
+    // of its segment, without work, so that no other waits for it.
+    const int w = warp >> 2;   // stream
+    const int row = tid & 127; // its lane of tensor memory
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes;
     const float sc = P.scale_log2;
-    const int spr = P.N * P.rep;
-    int kb = 0, seg = 0, sp = 0;  // blocks before this segment; steps of this stream
+    const bool tree = P.plan.hdr[kHdrTree] != 0;
+    int left = P.plan.start[blockIdx.x + 1].w - P.plan.start[blockIdx.x].w;
+    int g0 = 0, kb = 0, qt = 0, seg = 0;  // steps, blocks, query tiles and segments before
     bool ok = true;
-    for (; ok && wk.more(); wk.next(P), ++seg) {
-      const KvTile& t = wk.t;
-      const bool rows2 = t.rows > 128;
-      // queries of this unit, 16 bytes a copy: a lane finds its row's address,
-      // the warp's copies are all in flight at once (one after the other they
-      // took 14 us a unit)
-      {
-        constexpr int kPer = D / 8;              // copies of a row
-        constexpr int kRows = 32 / kPer;         // rows of one step of the warp
-        const int cnt = rows2 ? 32 : 16;         // rows of this warp
-        const int r0 = rows2 ? 32 * (warp & 3) : 64 * w + 16 * (warp & 3);
-        unsigned char* dst = smem + (rows2 ? w : 0) * R::kTile;
-        const int lr = (rows2 ? 128 * w : 0) + r0 + lane;
-        int64_t mine = -1;
-        if (lane < cnt && lr < t.rows) {
-          const int rr = t.row0 + lr, i = t.i0 + rr / spr, in = rr % spr;
-          mine = ((int64_t)i * P.N + in / P.rep) * P.q_stride + (int64_t)(wk.head * P.rep + in % P.rep) * D;
-        }
-        const int pc = lane % kPer;
-        for (int x = 0; x < cnt; x += kRows) {
-          const int e = x + lane / kPer, rt = r0 + e;
-          const int64_t from = __shfl_sync(kFullMask, mine, e);
-          if (from >= 0)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             smem_u32(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4))),
-                         "l"(P.q + from * 2 + pc * 16)
-                         : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (tid == 0) ctl->bad = 0;
-        fence_async_smem();
-        tc_fence_before();  // the last segment's reads of tensor memory
-        mbar_arrive(&ctl->q_full);
+    for (; left > 0; ++seg) {
+      ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
+      if (named_any(4, 256, !ok)) {
+        ok = false;
+        break;
       }
-      // this thread's row: what it sees of the new tokens
-      const int r = rows2 ? 128 * w + row : row;
-      const int rr = t.row0 + r;
-      const int i = t.i0 + rr / spr, node = rr % spr / P.rep, hq = wk.head * P.rep + rr % P.rep;
-      const bool in = r < t.rows;
-      int base = t.kend, lim = t.kend, ntok = 0;
+      const Segment& sg = ctl->seg[seg & 3];  // the loader is two segments ahead at most
+      if (tid == 0) {
+        mbar_arrive(&ctl->q_empty[qt & 1]);
+        if (sg.t.rows > 128) mbar_arrive(&ctl->q_empty[(qt + 1) & 1]);
+      }
+      const int nb = sg.nb, trows = sg.t.rows, kind = sg.t.kind, kend = sg.t.kend, ctx = sg.t.ctx;
+      const int kseg = sg.t.kbeg + sg.blk * kKeyBlock;
+      const bool rows2 = trows > 128;
+      const int items = rows2 ? 2 * nb : nb;
+      const int x0 = (w - g0) & 1;                 // this stream's first step of the segment
+      const int r = row + (rows2 ? 128 * x0 : 0);  // this thread's row of the unit
+      const bool live = r < trows;
+      const bool busy = r - lane < trows;
+      // what the row sees: keys before lim, and a tree's nodes
+      int lim = kend;
       uint32_t see = 0;
-      if (in) {
-        ntok = P.plan.seq[i].ntok;
-        if (!t.prefix) {
-          base = P.plan.seq[i].base;
-          if (tree) {
-            see = (uint32_t)P.plan.node[(int64_t)i * P.N + node].y;
-            lim = base;
-          } else {
-            lim = min(t.kend, base + node + 1);
-          }
+      const int base = sg.t.base;
+      if (live && kind != 1) {
+        const int rr = sg.t.row0 + r;
+        if (tree) {
+          see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + rr / P.rep].y;
+          lim = base;
+        } else {
+          lim = min(kend, base + rr / P.rep + 1);
         }
       }
-      const bool live = in && node < ntok;
-      const int ctx = t.prefix ? t.kend : P.plan.seq[t.i0].base;  // keys before it need no mask
-      const bool busy = (rows2 ? 128 * w : 0) + 32 * (warp & 3) < t.rows;
       float m = -INFINITY, l = 0.f;  // m in units of raw scores
-      const int items = rows2 ? 2 * wk.nb : wk.nb;
-      for (int x = w; x < items; x += 2, ++sp) {
+      for (int x = x0; x < items; x += 2) {
         const int b = rows2 ? x >> 1 : x;
-        const int k0 = t.kbeg + (wk.blk + b) * kKeyBlock;
+        const int k0 = kseg + b * kKeyBlock;
         const bool edge = k0 + kKeyBlock > ctx;
-        if (ok) ok = wait_for(&ctl->s_full[w], sp & 1, ctl, P.wait_ns);
+        if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
         if (ok && busy) {
           uint32_t s[128];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld32(mS, s);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(mS + 32 * q, s + 32 * q);
-          tmem_wait_ld();
-          if (edge) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld(s + 32 * q);
+            if (q < 3) tmem_ld32(mS + 32 * (q + 1), s + 32 * (q + 1));
+            if (edge) {
               const int ks = k0 + 32 * q;
               // bits of the 32 keys from ks on: those before lim, and a tree's
               uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
@@ -727,12 +892,9 @@ __global__ void __launch_bounds__(384, 1)
               for (int e = 0; e < 32; ++e)
                 if (!((bits >> e) & 1)) s[32 * q + e] = 0xff800000u;
             }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[32 * q + e]));
           }
-          float mx[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(s[q]);
-#pragma unroll
-          for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           float f = 1.f;
           if (m == -INFINITY) {
@@ -744,171 +906,142 @@ __global__ void __launch_bounds__(384, 1)
           if (x >= 2 && __any_sync(kFullMask, live && f != 1.f)) {
             l *= f;
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(mO + 32 * q, o);
-              tmem_wait_ld();
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(mO + 16 * q, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(mO + 32 * q, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(mO + 16 * q, o);
             }
           }
           const float off = m == -INFINITY ? 0.f : H::kOffset - m * sc;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t p[32];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = ex2_approx(fmaf(__uint_as_float(s[64 * q + 2 * e]), sc, off));
-              const float d = ex2_approx(fmaf(__uint_as_float(s[64 * q + 2 * e + 1]), sc, off));
-              sum[e & 3] += a + d;
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = unpack2(fma2(
+                  pack2(__uint_as_float(s[32 * q + 2 * e]), __uint_as_float(s[32 * q + 2 * e + 1])), sc2, off2));
+              const float a = ex2_approx(y.x), d = ex2_approx(y.y);
+              sum[e & 1] = add2(sum[e & 1], pack2(a, d));
               p[e] = H::pack(a, d);
             }
-            tmem_st32(mS + 32 * q, p);
+            tmem_st16(mS + 16 * q, p);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 t2 = unpack2(add2(sum[0], sum[1]));
+          l += t2.x + t2.y;
           tmem_wait_st();
         }
         if (edge) {
-          // values that no query of the unit sees become zeros, and so do
-          // infinities and NaN of new tokens, which only some see (0 * NaN
-          // would reach the others): those that do see them add them at the end
           const int t_v = 2 * (kb + b) + 1, st = t_v % R::kStages;
           if (ok) ok = wait_for(&ctl->full[st], (t_v / R::kStages) & 1, ctl, P.wait_ns);
-          if (ok && (!rows2 || w == 0)) {
-            constexpr int kPer = D / 8;
-            const int lo = max(ctx - k0, 0), hi = min(t.kend - k0, kKeyBlock);
-            unsigned char* v = ring + st * R::kTile;
-            bool found = false;
-            for (int e = row; e < (kKeyBlock - lo) * kPer; e += 128) {
-              const int r1 = lo + e / kPer, pc = e % kPer;
-              uint4* at = reinterpret_cast<uint4*>(v + (pc >> 3) * 16384 + r1 * 128 + (((pc & 7) ^ (r1 & 7)) << 4));
-              if (r1 >= hi) {
-                *at = uint4{0, 0, 0, 0};
-              } else {
-                uint4 u = *at;
-                uint32_t* a = reinterpret_cast<uint32_t*>(&u);
-                bool hit = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t lo16 = (a[k] & H::kExponent) == H::kExponent ? 0xffffu : 0u;
-                  const uint32_t hi16 = ((a[k] >> 16) & H::kExponent) == H::kExponent ? 0xffff0000u : 0u;
-                  hit |= (lo16 | hi16) != 0;
-                  a[k] &= ~(lo16 | hi16);
-                }
-                if (hit) *at = u;
-                found |= hit;
-              }
-            }
-            if (found) ctl->bad = 1;
-            fence_async_smem();
-          }
+          // (a unit of two row tiles: both streams use the values)
+          if (ok)
+            clean_values<T, D>(ring + st * R::kTile, max(ctx - k0, 0), min(kend - k0, kKeyBlock),
+                               rows2 ? row + 128 * w : row, rows2 ? 256 : 128, ctl);
           if (rows2) named_sync(3, 256);
           else named_sync(1 + w, 128);
         }
         tc_fence_before();
-        mbar_arrive(&ctl->p_full[w]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[w]);
       }
-      kb += wk.nb;
+      const bool both = !rows2 && items > 1;
+      if (!rows2) ctl->ml[128 * w + row] = {m, l};
       if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
-      ok = !named_any(4, 256, !ok);  // all threads of both streams decide alike
+      // all threads of both streams decide alike (and have the exchange)
+      ok = !named_any(4, 256, !ok);
       if (!ok) break;
       tc_fence_after();
-      const bool both = !rows2 && items > 1;
-      float2* ml = reinterpret_cast<float2*>(smem);  // the queries' place: they have been used
-      if (!rows2) {
-        ml[128 * w + row] = {m, l};
-        named_sync(4, 256);
-      }
       float f0 = 1.f, f1 = 0.f;
       if (!rows2) {
+        const float2 a = ctl->ml[128 * (g0 & 1) + row];
+        m = a.x;
+        l = a.y;
         if (both) {
-          const float2 a = ml[row], z = ml[128 + row];
+          const float2 z = ctl->ml[128 * (~g0 & 1) + row];
           m = fmaxf(a.x, z.x);
           const float mm = m == -INFINITY ? 0.f : m;
           f0 = ex2_approx((a.x - mm) * sc);
           f1 = ex2_approx((z.x - mm) * sc);
           l = a.y * f0 + z.y * f1;
-        } else {
-          m = ml[row].x;  // stream 0 had the only block
-          l = ml[row].y;
         }
       }
-      const int d0 = rows2 ? 0 : w * (D / 2), d1 = rows2 ? D : d0 + D / 2;
-      const bool direct = wk.whole() && P.plan.seq[t.i0].shared == 0;
-      float* part = nullptr;
+      // a unit of two row tiles: a thread its row's D sums; else the streams
+      // take half of the columns each, and add up both streams' sums
+      const bool direct = nb == sg.t.blocks && kind == 0;
+      const int head = sg.head, i0 = sg.t.i0, seq_row = sg.t.seq_row;
+      const bool bad = ctl->bad && kind != 1;
+      const int d0 = rows2 ? 0 : w * (D / 2), cols = rows2 ? D : D / 2;
+      const int rr = sg.t.row0 + r, i = i0 + rr / spr, node = rr % spr / P.rep;
+      const int64_t q_row = ((int64_t)i * P.N + node) * P.q_heads + head * P.rep + rr % P.rep;
       int64_t slot = 0;
       if (!direct) {
-        if (wk.whole()) {
-          slot = 2 * kKvCtas * kTileRows + (t.prefix ? P.plan.store : 0) +
-                 (((int64_t)i * P.N + node) * P.q_heads + hq);
-        } else {
-          // the first segment of a CTA's share, or its last
-          slot = (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + r;
-        }
-        part = P.plan.o + slot * D;
+        // a whole unit that is joined with others: the store of its kind; else
+        // the first segment of a CTA's share, or its last
+        slot = nb == sg.t.blocks ? 2 * kKvCtas * kTileRows + (kind == 1 ? P.plan.store : 0) + q_row
+                                 : (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + r;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      if (busy) {
-        const uint32_t a0 = tO + lanes + (rows2 ? 128 * w : 0);
-        for (int d = d0; d < d1; d += 32) {
-          uint32_t u[32];
-          float o[32];
-          tmem_ld32(a0 + d, u);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+      const uint32_t a0 = tO + lanes + 128 * (rows2 ? w : g0 & 1), a1 = tO + lanes + 128 * (~g0 & 1);
+      for (int d = 0; d < cols; d += 32) {
+        uint32_t u[32], v[32];
+        if (busy) {
+          tmem_ld32(a0 + d0 + d, u);
+          if (both) tmem_ld32(a1 + d0 + d, v);
+          tmem_wait_ld(u);
           if (both) {
-            tmem_ld32(a0 + 128 + d, u);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(u[e]) * f1;
+            for (int e = 0; e < 32; ++e)
+              u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
           }
-          if (live) {
-          if (ctl->bad && !t.prefix) {
-            // infinities and NaN that this row does see
-            for (int key = max(base, t.kbeg + wk.blk * kKeyBlock);
-                 key < min(t.kend, t.kbeg + (wk.blk + wk.nb) * kKeyBlock); ++key) {
-              if (!(key < lim || (see && key - base < 32 && ((see >> (key - base)) & 1)))) continue;
-              const int pg = c.table[(int64_t)P.plan.seq[i].row * c.max_pages + (key >> c.log_page)];
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  c.v + kv_offset(c, P.layer, pg, wk.head) + ((int64_t)(key & (c.page - 1)) * D + d) * 2);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t z = v[e];
-                if ((z & H::kExponent) == H::kExponent) o[2 * e] += H::lo(z);
-                if (((z >> 16) & H::kExponent) == H::kExponent) o[2 * e + 1] += H::hi(z);
-              }
-            }
-          }
-          if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(
-                P.out + ((((int64_t)i * P.N + node) * P.q_heads + hq) * D + d) * 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = {H::pack(o[8 * e] * inv, o[8 * e + 1] * inv), H::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                        H::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv), H::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv)};
-          } else {
-            float4* dst = reinterpret_cast<float4*>(part + d);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = {o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]};
-          }
-          }
-          __syncwarp();
         }
-        if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+        if (d + 32 >= cols) {  // O has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->o_free);
+        }
+        if (live) {
+          if (direct) {
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              h[e] = H::pack(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+            unsigned char* dst = P.out + (q_row * D + d0 + d) * 2;
+            store32(dst, h);
+            store32(dst + 32, h + 8);
+          } else {
+            float* dst = P.plan.o + slot * D + d0 + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store32(dst + 8 * e, u + 8 * e);
+          }
+        }
+        __syncwarp();
       }
-      // both streams are done with the exchange and the flag before new
-      // queries replace them
+      if (bad && live)
+        add_unclean<T>(P, seq_row, head, base, lim, see, max(ctx, kseg), min(kend, kseg + nb * kKeyBlock), d0, cols,
+                       direct ? P.out + (q_row * D + d0) * 2 : nullptr, P.plan.o + slot * D + d0);
+      if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+      // the exchange and the flag may be used again
       named_sync(4, 256);
+      if (bad && tid == 0) ctl->bad = 0;
+      g0 += items;
+      kb += nb;
+      qt += rows2 ? 2 : 1;
+      left -= nb;
     }
     if (!ok) {
       // the sequences of this and the following units have no result
-      for (; wk.more(); wk.next(P)) {
-        const int last = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / spr;
-        for (int k = wk.t.i0 + tid; k <= last; k += 256) P.plan.status[k] = SAMSPEC_ST_TIMEOUT;
-      }
+      int k = 0;
+      for (Walk wk(P); wk.more(); wk.next(P), ++k)
+        if (k >= seg) {
+          const int last = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / spr;
+          for (int j = wk.t.i0 + tid; j <= last; j += 256) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
+        }
       if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     }
   }
@@ -922,10 +1055,10 @@ __global__ void __launch_bounds__(384, 1)
 // partial results joined.  Rows that were written where they were computed are
 // passed over, those of no token become zeros.  A warp takes 8 rows: a lane
 // finds where one row's parts lie, then the warp adds up one row after the
-// other, the loads of up to 4 parts in flight at once.
-constexpr int kJoinRows = 8;
+// other, the loads of up to 4 parts in flight at once.  (Calls of few rows
+// give a warp fewer.)
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(AttendParams P) {
+__global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows) {
   using H = Type16<T>;
   constexpr int kPer = D / 32;
   struct alignas(4 * kPer) Vec {
@@ -933,13 +1066,13 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P) {
   };
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoinRows;
+  const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * warp_rows;
   if (r0 >= rows) return;
   // of lane's row: parts (-1: none to join, 0: zeros), and for the shared and
   // the own keys where the first part lies and where the others begin
   int parts = -1, first[2] = {0, 0}, rest[2] = {0, 0}, cnt[2] = {0, 0};
   const int64_t mine = r0 + lane;
-  if (lane < kJoinRows && mine < rows) {
+  if (lane < warp_rows && mine < rows) {
     const int hq = (int)(mine % P.q_heads);
     const int64_t tok = mine / P.q_heads;
     const int i = (int)(tok / P.N), node = (int)(tok % P.N);
@@ -1052,7 +1185,8 @@ int attend(const AttendParams& P, const CUtensorMap& mk, const CUtensorMap& mv, 
     return SAMSPEC_ECUDA;
   attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  join_kernel<T, D><<<(unsigned)((rows + 8 * kJoinRows - 1) / (8 * kJoinRows)), 256, 0, s>>>(P);
+  const int per = rows >= kKvCtas * 32 * 8 ? 8 : rows >= kKvCtas * 32 * 2 ? 2 : 1;
+  join_kernel<T, D><<<(unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s>>>(P, per);
   return launched();
 }
 

@@ -102,7 +102,11 @@ struct KvSeq {
 struct KvTile {
   int32_t i0, row0, rows;
   int32_t kbeg, kend;  // tokens
-  int32_t prefix;      // 1: keys that the group shares, every row sees them all
+  int32_t ctx;         // every row sees the keys before this one
+  int32_t base, ntok;  // of the sequence (own keys)
+  int32_t seq_row;     // the cache row whose pages are read
+  int32_t kind;        // 1: keys that the group shares, every row sees them all;
+                       // 2: own keys of a sequence whose group shares others
   int32_t blocks;      // key blocks
   int32_t cost0;       // cost of all heads of the tiles before
 };
