@@ -159,9 +159,11 @@ __global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
 // One CTA: what a group reads once, the units of work and their order, and
 // each persistent CTA's equal share of the key blocks.
 constexpr int kMinShared = 128;  // tokens: less is read by each sequence for itself
-// what a unit costs besides its blocks (its queries, the start and end of its
-// two streams), in blocks
-constexpr int kUnitCost = 2;
+// Costs, in blocks of a unit of one row tile (2600 clocks, by HBM): a block of
+// two row tiles (two steps of softmax on each warp), and what a unit costs
+// besides its blocks (the start and end of its two streams).
+constexpr int kUnitCost = 4;
+__device__ __forceinline__ int block_cost(const KvTile& t) { return t.rows > 128 ? 2 : 1; }
 
 __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __shared__ int part[32];
@@ -239,12 +241,14 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   for (int t0 = 0; t0 < tiles; t0 += 1024) {
     const int t = t0 + tid;
     int sum;
-    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks + kUnitCost) * c.kv_heads : 0, part, &sum);
+    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks * block_cost(P.plan.tile[t]) + kUnitCost) * c.kv_heads : 0,
+                              part, &sum);
     if (t < tiles) P.plan.tile[t].cost0 = cost + at;
     cost += sum;
   }
   __syncthreads();
-  const int ctas = min(kKvCtas, cost);  // at most one CTA begins at any cost
+  // costs of at least 2 lie between two shares: no two begin in one block
+  const int ctas = min(kKvCtas, (cost + 1) / 2);
   for (int x = tid; x <= ctas; x += 1024) {
     const int b = ctas ? (int)((int64_t)x * cost / ctas) : 0;
     int lo = 0, hi = tiles - 1;  // the last tile that begins at or before b
@@ -253,15 +257,23 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
       if (P.plan.tile[mid].cost0 <= b) lo = mid;
       else hi = mid - 1;
     }
-    // the cost b lies in: unit (lo, y), at its block z; w counts all blocks before
-    int4 s = {0, 0, 0, cost - kUnitCost * c.kv_heads * tiles};
+    // the share begins in unit (lo, y) at block z: the first of which no cost
+    // lies before b
+    int4 s = {tiles, 0, 0, 0};
     if (x < ctas) {
       const KvTile t = P.plan.tile[lo];
-      const int u = t.blocks + kUnitCost;
+      const int bc = block_cost(t), u = t.blocks * bc + kUnitCost;
       s.x = lo;
       s.y = (b - t.cost0) / u;
-      s.z = max((b - t.cost0) % u - kUnitCost, 0);
-      s.w = t.cost0 - kUnitCost * c.kv_heads * lo + s.y * t.blocks + s.z;
+      s.z = ((b - t.cost0) % u - kUnitCost + bc - 1) / bc;
+      if (s.z < 0) s.z = 0;
+      if (s.z == t.blocks) {  // behind the unit's last block
+        s.z = 0;
+        if (++s.y == c.kv_heads) {
+          s.y = 0;
+          ++s.x;
+        }
+      }
     }
     P.plan.start[x] = s;
   }
@@ -275,10 +287,25 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
 }
 
 // ---- attention ---------------------------------------------------------------
+// x / d for 0 <= x < 2^31 by a multiplication: ceil(2^(31 + s) / d), s the
+// bits of d - 1, is off by less than d / 2^s <= 1, so the quotient by less
+// than x / 2^31 < 1 part of 1 / d
+struct Divider {
+  uint32_t mul, shift;
+  explicit Divider(uint32_t d = 1) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    shift = 31 + s;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
+};
+
 struct AttendParams {
   KvView c;
   PlanView plan;
   int layer, n, N, q_heads, rep;
+  Divider rep_div;
   const unsigned char* q;
   int64_t q_stride;
   float scale_log2;  // scale * log2(e), positive
@@ -431,13 +458,13 @@ struct Type16<__half> {
 // the matrix instructions read.
 struct Segment {  // what the queries' loader hands on of a segment
   KvTile t;
-  int32_t head, blk, nb, pad;
+  int32_t head, blk, nb, last;
 };
 struct Ctl {
   uint64_t full[11], empty[11], s_full[2], p_full[2], q_full[2], q_empty[2], o_done, o_free, drain;
   uint32_t tmem;
   int32_t abort, bad;
-  float2 ml[256];  // running maxima and sums that the streams exchange
+  float x[2][2][128];  // maxima and sums that are exchanged: stream, half of the keys, row
   alignas(16) Segment seg[4];
 };
 template <int D>
@@ -482,30 +509,39 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// A CTA's share of the work: blocks of consecutive units (tile, key head).
+// A CTA's share of the work: blocks of consecutive units (tile, key head), up
+// to where the next one's begins.
 struct Walk {
-  int tile, head, blk, left;
+  int tile, head, blk;
+  int4 end;
   KvTile t;
   int nb;  // blocks of the segment in hand
   __device__ __forceinline__ Walk(const AttendParams& P) {
     const int4 a = P.plan.start[blockIdx.x];
-    left = P.plan.start[blockIdx.x + 1].w - a.w;
+    end = P.plan.start[blockIdx.x + 1];
     tile = a.x;
     head = a.y;
     blk = a.z;
     load(P);
   }
   __device__ __forceinline__ void load(const AttendParams& P) {
-    if (left > 0) {
+    if (more()) {
       const int4* s = reinterpret_cast<const int4*>(P.plan.tile + tile);
       const int4 a = s[0], b = s[1], c = s[2];
       t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-      nb = min(left, t.blocks - blk);
+      nb = (tile == end.x && head == end.y ? end.z : t.blocks) - blk;
     }
   }
-  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool more() const {
+    return tile < end.x || (tile == end.x && (head < end.y || (head == end.y && blk < end.z)));
+  }
+  // is the segment in hand the last?
+  __device__ __forceinline__ bool final_one(const AttendParams& P) const {
+    const bool wrap = head + 1 == P.c.kv_heads;
+    return (tile == end.x && head == end.y) ||
+           (end.z == 0 && tile + wrap == end.x && (wrap ? 0 : head + 1) == end.y);
+  }
   __device__ __forceinline__ void next(const AttendParams& P) {
-    left -= nb;
     blk = 0;
     if (++head == P.c.kv_heads) {
       head = 0;
@@ -515,6 +551,11 @@ struct Walk {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Two floats in one instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -583,11 +624,13 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
                                          int from, int to, int d0, int cols, unsigned char* out, float* sums) {
   using H = Type16<T>;
   const KvView& c = P.c;
+#pragma unroll 1
   for (int key = from; key < to; ++key) {
     if (!(key < lim || (key >= base && key - base < 32 && ((see >> (key - base)) & 1)))) continue;
     const int pg = c.table[(int64_t)seq_row * c.max_pages + (key >> c.log_page)];
     const uint32_t* v = reinterpret_cast<const uint32_t*>(
         c.v + kv_offset(c, P.layer, pg, head) + ((int64_t)(key & (c.page - 1)) * c.head_dim + d0) * 2);
+#pragma unroll 1
     for (int e = 0; e < cols / 2; ++e) {
       const uint32_t z = v[e];
       const bool lo = (z & H::kExponent) == H::kExponent, hi = ((z >> 16) & H::kExponent) == H::kExponent;
@@ -603,9 +646,11 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
   }
 }
 
-// One persistent CTA an SM, 12 warps.  Warp 8 loads pages by TMA, warp 9
-// issues matrix products, warps 10 and 11 load queries, two warpgroups do the
-// softmax, a thread a row.
+// One persistent CTA an SM, 20 warps.  Warp 16 loads pages by TMA, warp 17
+// issues matrix products, warps 18 and 19 load queries, two pairs of
+// warpgroups do the softmax: a pair has a stream, each of its two halves of a
+// block's keys, a thread a row of them.  (One warpgroup a stream, a thread all
+// 128 keys of its row, took 2700 clocks a step where the pair takes ...)
 //
 // A step is one block of 128 keys against 128 query rows: S = Q K^T (both in
 // shared memory, S in tensor memory), P = exp2(S - m) rounded to 16 bits over
@@ -623,7 +668,7 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
 // memory time: at 128 keys * D * 4 bytes a step HBM takes about 2800 clocks an
 // SM, the two products 1024, a warp's softmax about 1500 with two in flight.
 template <typename T, int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
   using R = Ring<D>;
@@ -638,7 +683,7 @@ __global__ void __launch_bounds__(384, 1)
     if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     return;
   }
-  if (warp == 9) tmem_alloc(&ctl->tmem, 512);
+  if (warp == 17) tmem_alloc(&ctl->tmem, 512);
   if (tid == 0) {
     for (int s = 0; s < R::kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
@@ -646,12 +691,12 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl->s_full[w], 1);
-      mbar_init(&ctl->p_full[w], 4);
+      mbar_init(&ctl->p_full[w], 8);
       mbar_init(&ctl->q_full[w], 2);
       mbar_init(&ctl->q_empty[w], 2);  // its products are done, its segment has been seen
     }
     mbar_init(&ctl->o_done, 1);
-    mbar_init(&ctl->o_free, 8);
+    mbar_init(&ctl->o_free, 16);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     ctl->bad = 0;
@@ -662,12 +707,11 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   const uint32_t tS = tmem, tO = tmem + 256;  // streams 128 columns apart
-  const int spr = P.N * P.rep;
 
-  // registers: 384 * 168 at launch = 256 * 216 + 128 * 72
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
+  // registers: 640 * 96 at launch = 512 * 104 + 128 * 64
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 16) {
       // ---- pages to the ring ----
       int kt = 0;  // tiles requested
       bool ok = true;
@@ -706,7 +750,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok)
         for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
           drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // ---- matrix products ----
       if (lane == 0) {
         const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
@@ -727,8 +771,8 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
           const uint64_t vd = tile_desc(ring + st * R::kTile, 16384);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows
-            mma_ts(tO + 128 * w, tS + 128 * w + 8 * k, vd + k * (2048 >> 4), id_o, !v_first || k > 0);
+          for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows; P's halves lie 64 columns apart
+            mma_ts(tO + 128 * w, tS + 128 * w + (k / 4) * 64 + (k % 4) * 8, vd + k * (2048 >> 4), id_o, !v_first || k > 0);
           if (v_last) mma_commit(&ctl->empty[st]);
           if (v_end) mma_commit(&ctl->o_done);
           v_tile = -1;
@@ -790,13 +834,14 @@ __global__ void __launch_bounds__(384, 1)
           constexpr int kRows = 32 / kPer;  // rows of one step of the warp
           unsigned char* dst = smem + (qt & 1) * R::kTile;
           const int pc = lane % kPer;
-#pragma unroll
+#pragma unroll 1
           for (int z = 0; z < 2; ++z) {
-            const int r0 = 64 * (warp - 10) + 32 * z, lr = 128 * half + r0 + lane;
+            const int r0 = 64 * (warp - 18) + 32 * z, lr = 128 * half + r0 + lane;
             int64_t mine = -1;
             if (lr < wk.t.rows) {
-              const int rr = wk.t.row0 + lr, i = wk.t.i0 + rr / spr, in = rr % spr;
-              mine = ((int64_t)i * P.N + in / P.rep) * P.q_stride + (int64_t)(wk.head * P.rep + in % P.rep) * D;
+              // (sequences' tokens follow one another)
+              const int rr = wk.t.row0 + lr, tok = P.rep_div(rr);
+              mine = ((int64_t)wk.t.i0 * P.N + tok) * P.q_stride + (int64_t)(wk.head * P.rep + rr - tok * P.rep) * D;
             }
 #pragma unroll
             for (int y = 0; y < 32; y += kRows) {
@@ -809,8 +854,9 @@ __global__ void __launch_bounds__(384, 1)
                              : "memory");
             }
           }
-          if (warp == 10 && lane == 0 && half == 0)
-            ctl->seg[seg & 3] = {wk.t, wk.head, wk.blk, wk.nb, 0};
+          if (warp == 18 && lane == 0 && half == 0) {
+            ctl->seg[seg & 3] = {wk.t, wk.head, wk.blk, wk.nb, wk.final_one(P)};
+          }
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_smem();
           __syncwarp();
@@ -819,22 +865,23 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- softmax ----
     // A thread that gives up keeps taking part in every barrier and arrival
     // of its segment, without work, so that no other waits for it.
-    const int w = warp >> 2;   // stream
-    const int row = tid & 127; // its lane of tensor memory
+    const int w = warp >> 3, half = (warp >> 2) & 1;  // stream, half of the keys
+    const int row = (warp & 3) * 32 + lane;           // its lane of tensor memory
+    const int pair = 1 + w * 4 + (warp & 3);          // barrier with the other half's warp
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes;
+    const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes + half * (D / 2);
     const float sc = P.scale_log2;
     const bool tree = P.plan.hdr[kHdrTree] != 0;
-    int left = P.plan.start[blockIdx.x + 1].w - P.plan.start[blockIdx.x].w;
     int g0 = 0, kb = 0, qt = 0, seg = 0;  // steps, blocks, query tiles and segments before
+    bool last = !Walk(P).more();
     bool ok = true;
-    for (; left > 0; ++seg) {
+    for (; !last; ++seg) {
       ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
-      if (named_any(4, 256, !ok)) {
+      if (named_any(12, 512, !ok)) {
         ok = false;
         break;
       }
@@ -843,6 +890,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&ctl->q_empty[qt & 1]);
         if (sg.t.rows > 128) mbar_arrive(&ctl->q_empty[(qt + 1) & 1]);
       }
+      const bool ends = sg.last;
       const int nb = sg.nb, trows = sg.t.rows, kind = sg.t.kind, kend = sg.t.kend, ctx = sg.t.ctx;
       const int kseg = sg.t.kbeg + sg.blk * kKeyBlock;
       const bool rows2 = trows > 128;
@@ -852,19 +900,19 @@ __global__ void __launch_bounds__(384, 1)
       const bool live = r < trows;
       const bool busy = r - lane < trows;
       // what the row sees: keys before lim, and a tree's nodes
+      const int rr = sg.t.row0 + r, tok = P.rep_div(rr);
+      const int base = sg.t.base;
       int lim = kend;
       uint32_t see = 0;
-      const int base = sg.t.base;
       if (live && kind != 1) {
-        const int rr = sg.t.row0 + r;
         if (tree) {
-          see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + rr / P.rep].y;
+          see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + tok].y;
           lim = base;
         } else {
-          lim = min(kend, base + rr / P.rep + 1);
+          lim = min(kend, base + tok + 1);
         }
       }
-      float m = -INFINITY, l = 0.f;  // m in units of raw scores
+      float m = -INFINITY, l = 0.f;  // m in units of raw scores; l of this half's keys
       for (int x = x0; x < items; x += 2) {
         const int b = rows2 ? x >> 1 : x;
         const int k0 = kseg + b * kKeyBlock;
@@ -872,68 +920,95 @@ __global__ void __launch_bounds__(384, 1)
         if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
-        if (ok && busy) {
-          uint32_t s[128];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld32(mS, s);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_wait_ld(s + 32 * q);
-            if (q < 3) tmem_ld32(mS + 32 * (q + 1), s + 32 * (q + 1));
+        if (busy) {
+          // scores are read twice: holding all 64 between the maximum and the
+          // exponentials would take more registers than there are, and what is
+          // spilled goes to L2 (shared memory leaves no L1)
+          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+          float top = -INFINITY;
+          if (ok) {
             if (edge) {
-              const int ks = k0 + 32 * q;
-              // bits of the 32 keys from ks on: those before lim, and a tree's
-              uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
-              if (see) {
-                const int d = base - ks;
-                bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int ks = k0 + 64 * half + 32 * q;
+                // bits of the 32 keys from ks on: those before lim, and a tree's
+                uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
+                if (see) {
+                  const int d = base - ks;
+                  bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
+                }
+                seen[q] = bits;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t s[32];
+              tmem_ld32(mS + 64 * half + 32 * q, s);
+              tmem_wait_ld(s);
+              if (edge) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((seen[q] >> e) & 1)) s[e] = 0xff800000u;
+              }
+              float mx[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+              for (int e = 0; e < 12; ++e)
+                mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[8 + 2 * e]), __uint_as_float(s[9 + 2 * e]));
+              top = max3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            }
+            ctl->x[w][half][row] = top;
+          }
+          named_sync(pair, 64);
+          if (ok) {
+            top = fmaxf(top, ctl->x[w][half ^ 1][row]);
+            float f = 1.f;
+            if (m == -INFINITY) {
+              m = top;  // nothing of weight has been added up so far
+            } else if ((top - m) * sc > H::kLazy) {
+              f = ex2_approx((m - top) * sc);
+              m = top;
+            }
+            if (x >= 2 && __any_sync(kFullMask, live && f != 1.f)) {
+              l *= f;
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[16];
+                tmem_ld16(mO + 16 * q, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(mO + 16 * q, o);
+              }
+            }
+            const float off = m == -INFINITY ? 0.f : H::kOffset - m * sc;
+            const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t s[32], p[16];
+              tmem_ld32(mS + 64 * half + 32 * q, s);
+              tmem_wait_ld(s);
+              if (edge) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((seen[q] >> e) & 1)) s[e] = 0xff800000u;
               }
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((bits >> e) & 1)) s[32 * q + e] = 0xff800000u;
+              for (int e = 0; e < 16; ++e) {
+                const float2 y =
+                    unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, off2));
+                const float a = ex2_approx(y.x), d = ex2_approx(y.y);
+                sum[e & 1] = add2(sum[e & 1], pack2(a, d));
+                p[e] = H::pack(a, d);
+              }
+              tmem_st16(mS + 64 * half + 16 * q, p);
             }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[32 * q + e]));
+            const float2 t2 = unpack2(add2(sum[0], sum[1]));
+            l += t2.x + t2.y;
+            tmem_wait_st();
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          float f = 1.f;
-          if (m == -INFINITY) {
-            m = top;  // nothing of weight has been added up so far
-          } else if ((top - m) * sc > H::kLazy) {
-            f = ex2_approx((m - top) * sc);
-            m = top;
-          }
-          if (x >= 2 && __any_sync(kFullMask, live && f != 1.f)) {
-            l *= f;
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16(mO + 16 * q, o);
-              tmem_wait_ld16(o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(mO + 16 * q, o);
-            }
-          }
-          const float off = m == -INFINITY ? 0.f : H::kOffset - m * sc;
-          const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = unpack2(fma2(
-                  pack2(__uint_as_float(s[32 * q + 2 * e]), __uint_as_float(s[32 * q + 2 * e + 1])), sc2, off2));
-              const float a = ex2_approx(y.x), d = ex2_approx(y.y);
-              sum[e & 1] = add2(sum[e & 1], pack2(a, d));
-              p[e] = H::pack(a, d);
-            }
-            tmem_st16(mS + 16 * q, p);
-          }
-          const float2 t2 = unpack2(add2(sum[0], sum[1]));
-          l += t2.x + t2.y;
-          tmem_wait_st();
         }
         if (edge) {
           const int t_v = 2 * (kb + b) + 1, st = t_v % R::kStages;
@@ -941,43 +1016,46 @@ __global__ void __launch_bounds__(384, 1)
           // (a unit of two row tiles: both streams use the values)
           if (ok)
             clean_values<T, D>(ring + st * R::kTile, max(ctx - k0, 0), min(kend - k0, kKeyBlock),
-                               rows2 ? row + 128 * w : row, rows2 ? 256 : 128, ctl);
-          if (rows2) named_sync(3, 256);
-          else named_sync(1 + w, 128);
+                               rows2 ? tid : tid & 255, rows2 ? 512 : 256, ctl);
+          if (rows2) named_sync(11, 512);
+          else named_sync(9 + w, 256);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_full[w]);
       }
-      const bool both = !rows2 && items > 1;
-      if (!rows2) ctl->ml[128 * w + row] = {m, l};
       if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
-      // all threads of both streams decide alike (and have the exchange)
-      ok = !named_any(4, 256, !ok);
+      // the streams' maxima, then the halves' sums; all threads decide alike
+      // whether to go on
+      const bool both = !rows2 && items > 1;
+      ctl->x[w][half][row] = m;
+      ok = !named_any(12, 512, !ok);
       if (!ok) break;
       tc_fence_after();
+      const int wa = rows2 ? w : g0 & 1;  // the stream of the row's first step
       float f0 = 1.f, f1 = 0.f;
       if (!rows2) {
-        const float2 a = ctl->ml[128 * (g0 & 1) + row];
-        m = a.x;
-        l = a.y;
+        const float ma = ctl->x[wa][0][row];
+        m = ma;
         if (both) {
-          const float2 z = ctl->ml[128 * (~g0 & 1) + row];
-          m = fmaxf(a.x, z.x);
+          const float mb = ctl->x[wa ^ 1][0][row];
+          m = fmaxf(ma, mb);
           const float mm = m == -INFINITY ? 0.f : m;
-          f0 = ex2_approx((a.x - mm) * sc);
-          f1 = ex2_approx((z.x - mm) * sc);
-          l = a.y * f0 + z.y * f1;
+          f0 = ex2_approx((ma - mm) * sc);
+          f1 = ex2_approx((mb - mm) * sc);
         }
       }
-      // a unit of two row tiles: a thread its row's D sums; else the streams
-      // take half of the columns each, and add up both streams' sums
+      named_sync(12, 512);
+      ctl->x[w][half][row] = l;
+      named_sync(12, 512);
+      l = (ctl->x[wa][0][row] + ctl->x[wa][1][row]) * f0;
+      if (both) l += (ctl->x[wa ^ 1][0][row] + ctl->x[wa ^ 1][1][row]) * f1;
+      // a unit of two row tiles: a warpgroup half of its rows' sums; else each
+      // of the four a quarter, both streams' sums added up
       const bool direct = nb == sg.t.blocks && kind == 0;
-      const int head = sg.head, i0 = sg.t.i0, seq_row = sg.t.seq_row;
+      const int head = sg.head, seq_row = sg.t.seq_row;
       const bool bad = ctl->bad && kind != 1;
-      const int d0 = rows2 ? 0 : w * (D / 2), cols = rows2 ? D : D / 2;
-      const int rr = sg.t.row0 + r, i = i0 + rr / spr, node = rr % spr / P.rep;
-      const int64_t q_row = ((int64_t)i * P.N + node) * P.q_heads + head * P.rep + rr % P.rep;
+      const int64_t q_row = ((int64_t)sg.t.i0 * P.N + tok) * P.q_heads + head * P.rep + rr - tok * P.rep;
       int64_t slot = 0;
       if (!direct) {
         // a whole unit that is joined with others: the store of its kind; else
@@ -986,38 +1064,38 @@ __global__ void __launch_bounds__(384, 1)
                                  : (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + r;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const uint32_t a0 = tO + lanes + 128 * (rows2 ? w : g0 & 1), a1 = tO + lanes + 128 * (~g0 & 1);
-      for (int d = 0; d < cols; d += 32) {
-        uint32_t u[32], v[32];
+      const int cols = rows2 ? D / 2 : D / 4, d0 = rows2 ? half * (D / 2) : (2 * w + half) * (D / 4);
+      const uint32_t a0 = tO + lanes + 128 * wa + d0, a1 = tO + lanes + 128 * (wa ^ 1) + d0;
+#pragma unroll 1
+      for (int d = 0; d < cols; d += 16) {
+        uint32_t u[16], v[16];
         if (busy) {
-          tmem_ld32(a0 + d0 + d, u);
-          if (both) tmem_ld32(a1 + d0 + d, v);
-          tmem_wait_ld(u);
+          tmem_ld16(a0 + d, u);
+          if (both) tmem_ld16(a1 + d, v);
+          tmem_wait_ld16(u);
           if (both) {
-            tmem_wait_ld(v);
+            tmem_wait_ld16(v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
           }
         }
-        if (d + 32 >= cols) {  // O has been read
+        if (d + 16 >= cols) {  // O has been read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->o_free);
         }
         if (live) {
           if (direct) {
-            uint32_t h[16];
+            uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
               h[e] = H::pack(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
-            unsigned char* dst = P.out + (q_row * D + d0 + d) * 2;
-            store32(dst, h);
-            store32(dst + 32, h + 8);
+            store32(P.out + (q_row * D + d0 + d) * 2, h);
           } else {
             float* dst = P.plan.o + slot * D + d0 + d;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) store32(dst + 8 * e, u + 8 * e);
+            store32(dst, u);
+            store32(dst + 8, u + 8);
           }
         }
         __syncwarp();
@@ -1025,22 +1103,22 @@ __global__ void __launch_bounds__(384, 1)
       if (bad && live)
         add_unclean<T>(P, seq_row, head, base, lim, see, max(ctx, kseg), min(kend, kseg + nb * kKeyBlock), d0, cols,
                        direct ? P.out + (q_row * D + d0) * 2 : nullptr, P.plan.o + slot * D + d0);
-      if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+      if (live && !direct && half == 0 && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
       // the exchange and the flag may be used again
-      named_sync(4, 256);
+      named_sync(12, 512);
       if (bad && tid == 0) ctl->bad = 0;
       g0 += items;
       kb += nb;
       qt += rows2 ? 2 : 1;
-      left -= nb;
+      last = ends;
     }
     if (!ok) {
       // the sequences of this and the following units have no result
       int k = 0;
       for (Walk wk(P); wk.more(); wk.next(P), ++k)
         if (k >= seg) {
-          const int last = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / spr;
-          for (int j = wk.t.i0 + tid; j <= last; j += 256) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
+          const int end = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / (P.N * P.rep);
+          for (int j = wk.t.i0 + tid; j <= end; j += 512) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
         }
       if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     }
@@ -1048,7 +1126,7 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_free(tmem, 512);
+  if (warp == 17) tmem_free(tmem, 512);
 }
 
 // Rows of units that were cut among CTAs, or that have a shared part: their
@@ -1088,18 +1166,20 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
         const int at = p ? x : (i - s.leader) * P.N * P.rep + x;
         const int ti = (p ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + at / kTileRows;
         const KvTile t = P.plan.tile[ti];
-        const int b0 = t.cost0 + h * (t.blocks + kUnitCost);  // the unit's costs begin
+        const int bc = block_cost(t);
+        const int b0 = t.cost0 + h * (t.blocks * bc + kUnitCost);  // the unit's costs begin
         // the CTAs that hold its first and its last block: the last that
         // begins at or before each
         const int c0 = (int)((((int64_t)b0 + kUnitCost + 1) * ctas - 1) / cost);
-        const int c1 = (int)((((int64_t)b0 + kUnitCost + t.blocks) * ctas - 1) / cost);
+        const int c1 = (int)((((int64_t)b0 + kUnitCost + (t.blocks - 1) * bc + 1) * ctas - 1) / cost);
         cnt[p] = c1 - c0 + 1;
         if (c0 == c1) {
           if (s.shared == 0) cnt[p] = 0;
           first[p] = (int)(2 * kKvCtas * kTileRows + (p ? 0 : P.plan.store) + mine);
         } else {
           // the first segment of a CTA's share, or its last
-          const bool begins = (int64_t)c0 * cost / ctas >= b0;
+          const int4 st = P.plan.start[c0];
+          const bool begins = st.x == ti && st.y == h && st.z == 0;
           first[p] = (2 * c0 + !begins) * kTileRows + at % kTileRows;
           rest[p] = 2 * (c0 + 1) * kTileRows + at % kTileRows;
         }
@@ -1183,7 +1263,7 @@ int attend(const AttendParams& P, const CUtensorMap& mk, const CUtensorMap& mv, 
   if (cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes) !=
       cudaSuccess)
     return SAMSPEC_ECUDA;
-  attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv);
+  attend_kernel<T, D><<<kKvCtas, 640, Ring<D>::kBytes, s>>>(P, mk, mv);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
   const int per = rows >= kKvCtas * 32 * 8 ? 8 : rows >= kKvCtas * 32 * 2 ? 2 : 1;
   join_kernel<T, D><<<(unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s>>>(P, per);
@@ -1259,6 +1339,7 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   P.N = N;
   P.q_heads = q_heads;
   P.rep = q_heads / P.c.kv_heads;
+  P.rep_div = Divider((uint32_t)P.rep);
   P.q = static_cast<const unsigned char*>(d_q);
   P.q_stride = q_stride;
   P.scale_log2 = scale * 1.4426950408889634f;

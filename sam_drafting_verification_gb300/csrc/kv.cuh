@@ -131,7 +131,7 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
   const int64_t suf = (N * rep + kTileRows - 1) / kTileRows * n;
   const int64_t pre = grouped ? ((int64_t)n * N * rep + kTileRows - 1) / kTileRows + n : 0;
   // costs are counted in 32 bits
-  const int64_t blocks = (int64_t)c.max_pages * c.page / kKeyBlock + 8;
+  const int64_t blocks = ((int64_t)c.max_pages * c.page / kKeyBlock + 2) * 2 + 4;
   if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
   p.max_tiles = (int32_t)(suf + pre);
   p.store = grouped ? (int64_t)n * N * q_heads : 0;
@@ -160,7 +160,7 @@ struct PlanView {
   int32_t* suf0;   // first tile of a sequence's own keys
   int32_t* pre0;   // first tile of a group's shared keys (at the leader)
   KvTile* tile;
-  int4* start;     // where each CTA's share begins: tile, head, block, its blocks
+  int4* start;     // where each CTA's share begins: tile, head, block
   float2* ml;      // partial results: running maximum (base 2) and sum ...
   float* o;        // ... and the sums of p v
   int32_t max_tiles;
