@@ -309,6 +309,7 @@ struct AttendParams {
   const unsigned char* q;
   int64_t q_stride;
   float scale_log2;  // scale * log2(e), positive
+  float lazy;        // kLazy in units of raw scores
   unsigned char* out;
   uint64_t wait_ns;
 };
@@ -393,6 +394,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -476,12 +482,15 @@ struct Ring {
   static_assert(kBytes <= 232448, "227 KB of a CTA");
 };
 
-constexpr uint64_t kDescSwizzle128 = (1ull << 46) | (2ull << 61);
-// matrix descriptor of a tile: strides in bytes between slabs (keys across,
-// for the values) and between groups of 8 rows
-__device__ __forceinline__ uint64_t tile_desc(const void* p, uint32_t slab) {
-  return kDescSwizzle128 | (uint64_t)((smem_u32(p) & 0x3ffff) >> 4) | ((uint64_t)(slab >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32);
+// Matrix descriptor of a tile: address and strides in units of 16 bytes,
+// 16384 bytes between slabs (keys across, for the values), 1024 between groups
+// of 8 rows, 128-byte swizzle.  Only the low word depends on the address.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(const void* p) { return (smem_u32(p) >> 4) | ((16384u >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(low), "r"(kDescHigh));
+  return r;
 }
 
 // A bounded wait: false once the CTA gives up.  The first thread whose wait
@@ -755,63 +764,70 @@ __global__ void __launch_bounds__(640, 1)
       if (lane == 0) {
         const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
         const uint32_t id_s = id | ((128 >> 3) << 17), id_o = id | ((D >> 3) << 17) | (1u << 16);
-        bool ok = true;
-        // the step whose product with V is still to be issued (-1: none): its
-        // ring tile, whether it begins an O, ends a use of the tile, a segment
-        int v_tile = -1, v_seg = 0;
-        bool v_first = false, v_wait = false, v_last = false, v_end = false;
-        int g = 0;  // steps issued
+        const uint32_t q_low = desc_low(smem), ring_low = desc_low(ring);
+        bool ok = true, last = !Walk(P).more();
+        // the step whose product with V is still to be issued: its ring stage
+        // (-1: none), the parity of that, and what goes with it
+        enum { kFirst = 1, kAwaitV = 2, kRelease = 4, kEnd = 8, kAwaitO = 16, kParityO = 32, kParityV = 64 };
+        int v_stage = -1;
+        uint32_t v_what = 0;
+        int g = 0;               // steps issued
+        int st = 0, par = 0;     // ring stage of the block's keys, its parity
         auto product = [&] {
-          const int w = (g - 1) & 1, st = v_tile % R::kStages;
+          const int w = (g - 1) & 1;
           ok = wait_for(&ctl->p_full[w], ((g - 1) >> 1) & 1, ctl, P.wait_ns);
-          if (ok && v_wait) ok = wait_for(&ctl->full[st], (v_tile / R::kStages) & 1, ctl, P.wait_ns);
+          if (v_what & kAwaitV) ok = ok && wait_for(&ctl->full[v_stage], (v_what & kParityV) != 0, ctl, P.wait_ns);
           // the last segment's O has to be read before this one's begins
-          if (ok && v_first && v_seg > 0) ok = wait_for(&ctl->o_free, (v_seg - 1) & 1, ctl, P.wait_ns);
+          if (v_what & kAwaitO) ok = ok && wait_for(&ctl->o_free, (v_what & kParityO) != 0, ctl, P.wait_ns);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t vd = tile_desc(ring + st * R::kTile, 16384);
+          const uint32_t vl = ring_low + v_stage * (R::kTile >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows; P's halves lie 64 columns apart
-            mma_ts(tO + 128 * w, tS + 128 * w + (k / 4) * 64 + (k % 4) * 8, vd + k * (2048 >> 4), id_o, !v_first || k > 0);
-          if (v_last) mma_commit(&ctl->empty[st]);
-          if (v_end) mma_commit(&ctl->o_done);
-          v_tile = -1;
+            mma_ts(tO + 128 * w, tS + 128 * w + (k / 4) * 64 + (k % 4) * 8, desc(vl + k * (2048 >> 4)), id_o,
+                   !(v_what & kFirst) || k > 0);
+          if (v_what & kRelease) mma_commit(&ctl->empty[v_stage]);
+          if (v_what & kEnd) mma_commit(&ctl->o_done);
+          v_stage = -1;
         };
-        int kt = 0, qt = 0, seg = 0;
-        for (Walk wk(P); ok && wk.more(); wk.next(P), ++seg) {
-          const bool rows2 = wk.t.rows > 128;
-          const int items = rows2 ? 2 * wk.nb : wk.nb;
-          for (int q = 0; ok && q < (rows2 ? 2 : 1); ++q)
-            ok = wait_for(&ctl->q_full[(qt + q) & 1], ((qt + q) >> 1) & 1, ctl, P.wait_ns);
+        for (int seg = 0, qt = 0; ok && !last; ++seg) {
+          ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
+          if (!ok) break;
+          const int nb = ctl->seg[seg & 3].nb;
+          const bool rows2 = ctl->seg[seg & 3].t.rows > 128;
+          last = ctl->seg[seg & 3].last;
+          if (rows2) ok = wait_for(&ctl->q_full[(qt + 1) & 1], ((qt + 1) >> 1) & 1, ctl, P.wait_ns);
+          const int items = rows2 ? 2 * nb : nb;
           for (int x = 0; ok && x < items; ++x, ++g) {
-            const int w = g & 1, half = rows2 ? x & 1 : 0, b = rows2 ? x >> 1 : x;
-            const int t = kt + 2 * b, st = t % R::kStages;
-            if (half == 0) ok = wait_for(&ctl->full[st], (t / R::kStages) & 1, ctl, P.wait_ns);
+            const int w = g & 1, half = rows2 ? x & 1 : 0;
+            const bool done = !rows2 || half == 1;  // with the block's keys
+            if (half == 0) ok = wait_for(&ctl->full[st], par, ctl, P.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = tile_desc(smem + ((qt + half) & 1) * R::kTile, 16384);
-            const uint64_t kd = tile_desc(ring + st * R::kTile, 16384);
+            const uint32_t ql = q_low + ((qt + half) & 1) * (R::kTile >> 4), kl = ring_low + st * (R::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t at = (k / 4) * (16384 >> 4) + (k % 4) * 2;  // 16 elements along a row
-              mma_ss(tS + 128 * w, qd + at, kd + at, id_s, k > 0);
+              mma_ss(tS + 128 * w, desc(ql + at), desc(kl + at), id_s, k > 0);
             }
             mma_commit(&ctl->s_full[w]);
-            const bool last = !rows2 || half == 1;
-            if (last) mma_commit(&ctl->empty[st]);
-            if (x + 1 >= items - rows2) mma_commit(&ctl->q_empty[(qt + half) & 1]);
-            if (v_tile >= 0) product();
-            v_tile = t + 1;
-            v_seg = seg;
-            v_first = x < 2;
-            v_wait = half == 0;
-            v_last = last;
-            v_end = x == items - 1;
+            if (done) mma_commit(&ctl->empty[st]);
+            if (x + 1 >= items - (int)rows2) mma_commit(&ctl->q_empty[(qt + half) & 1]);
+            if (v_stage >= 0) product();
+            int vs = st + 1, vp = par;
+            if (vs == R::kStages) vs = 0, vp ^= 1;
+            v_stage = vs;
+            v_what = (x < 2 ? kFirst | (seg > 0 ? kAwaitO | ((seg - 1) & 1 ? kParityO : 0) : 0) : 0) |
+                     (half == 0 ? kAwaitV : 0) | (done ? kRelease : 0) | (x == items - 1 ? kEnd : 0) |
+                     (vp ? kParityV : 0);
+            if (done) {
+              st = vs + 1, par = vp;
+              if (st == R::kStages) st = 0, par ^= 1;
+            }
           }
-          kt += 2 * wk.nb;
           qt += rows2 ? 2 : 1;
         }
-        if (ok && v_tile >= 0) product();
+        if (ok && v_stage >= 0) product();
         if (!ok) {
           mma_commit(&ctl->drain);
           drain_wait(&ctl->drain, 0);
@@ -843,7 +859,7 @@ __global__ void __launch_bounds__(640, 1)
               const int rr = wk.t.row0 + lr, tok = P.rep_div(rr);
               mine = ((int64_t)wk.t.i0 * P.N + tok) * P.q_stride + (int64_t)(wk.head * P.rep + rr - tok * P.rep) * D;
             }
-#pragma unroll
+#pragma unroll 4
             for (int y = 0; y < 32; y += kRows) {
               const int e = y + lane / kPer, rt = r0 + e;
               const int64_t from = __shfl_sync(kFullMask, mine, e);
@@ -890,33 +906,35 @@ __global__ void __launch_bounds__(640, 1)
         mbar_arrive(&ctl->q_empty[qt & 1]);
         if (sg.t.rows > 128) mbar_arrive(&ctl->q_empty[(qt + 1) & 1]);
       }
-      const bool ends = sg.last;
-      const int nb = sg.nb, trows = sg.t.rows, kind = sg.t.kind, kend = sg.t.kend, ctx = sg.t.ctx;
-      const int kseg = sg.t.kbeg + sg.blk * kKeyBlock;
-      const bool rows2 = trows > 128;
-      const int items = rows2 ? 2 * nb : nb;
-      const int x0 = (w - g0) & 1;                 // this stream's first step of the segment
-      const int r = row + (rows2 ? 128 * x0 : 0);  // this thread's row of the unit
-      const bool live = r < trows;
-      const bool busy = r - lane < trows;
-      // what the row sees: keys before lim, and a tree's nodes
-      const int rr = sg.t.row0 + r, tok = P.rep_div(rr);
-      const int base = sg.t.base;
-      int lim = kend;
+      const bool rows2 = sg.t.rows > 128;
+      const int items = rows2 ? 2 * sg.nb : sg.nb;
+      const int x0 = (w - g0) & 1;  // this stream's first step of the segment
+      // what the row sees: keys before lim, and a tree's nodes; the first step
+      // whose keys not every row sees
+      bool live, busy;
+      int lim, x_edge;
       uint32_t see = 0;
-      if (live && kind != 1) {
-        if (tree) {
-          see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + tok].y;
-          lim = base;
-        } else {
-          lim = min(kend, base + tok + 1);
+      {
+        const int r = row + (rows2 ? 128 * x0 : 0), tok = P.rep_div(sg.t.row0 + r);  // this thread's row
+        live = r < sg.t.rows;
+        busy = r - lane < sg.t.rows;
+        lim = sg.t.kend;
+        if (live && sg.t.kind != 1) {
+          if (tree) {
+            see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + tok].y;
+            lim = sg.t.base;
+          } else {
+            lim = min(lim, sg.t.base + tok + 1);
+          }
         }
+        const int before = sg.t.ctx - sg.t.kbeg - sg.blk * kKeyBlock;
+        x_edge = (before > 0 ? before / kKeyBlock : 0) * (rows2 ? 2 : 1);
       }
-      float m = -INFINITY, l = 0.f;  // m in units of raw scores; l of this half's keys
+      // m in units of raw scores, and how far they may go before it moves; the
+      // exponent's constant; l of this half's keys
+      float m = -INFINITY, reach = -INFINITY, off = 0.f, l = 0.f;
       for (int x = x0; x < items; x += 2) {
-        const int b = rows2 ? x >> 1 : x;
-        const int k0 = kseg + b * kKeyBlock;
-        const bool edge = k0 + kKeyBlock > ctx;
+        const bool edge = x >= x_edge;
         if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
@@ -930,80 +948,86 @@ __global__ void __launch_bounds__(640, 1)
             if (edge) {
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const int ks = k0 + 64 * half + 32 * q;
+                const int ks = sg.t.kbeg + (sg.blk + (rows2 ? x >> 1 : x)) * kKeyBlock + 64 * half + 32 * q;
                 // bits of the 32 keys from ks on: those before lim, and a tree's
                 uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
                 if (see) {
-                  const int d = base - ks;
+                  const int d = sg.t.base - ks;
                   bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
                 }
                 seen[q] = bits;
               }
             }
+            uint32_t s[2][16];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            tmem_ld16(mS + 64 * half, s[0]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t s[32];
-              tmem_ld32(mS + 64 * half + 32 * q, s);
-              tmem_wait_ld(s);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t(&y)[16] = s[q & 1];
+              tmem_wait_ld16(y);
+              if (q < 3) tmem_ld16(mS + 64 * half + 16 * (q + 1), s[(q + 1) & 1]);
               if (edge) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((seen[q] >> e) & 1)) s[e] = 0xff800000u;
+                for (int e = 0; e < 16; ++e)
+                  if (!((seen[q / 2] >> (16 * (q & 1) + e)) & 1)) y[e] = 0xff800000u;
               }
-              float mx[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-#pragma unroll
-              for (int e = 0; e < 12; ++e)
-                mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[8 + 2 * e]), __uint_as_float(s[9 + 2 * e]));
-              top = max3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              for (int e = 0; e < 8; ++e)
+                mx[e & 3] = max3(mx[e & 3], __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
             }
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             ctl->x[w][half][row] = top;
           }
           named_sync(pair, 64);
           if (ok) {
             top = fmaxf(top, ctl->x[w][half ^ 1][row]);
-            float f = 1.f;
-            if (m == -INFINITY) {
-              m = top;  // nothing of weight has been added up so far
-            } else if ((top - m) * sc > H::kLazy) {
-              f = ex2_approx((m - top) * sc);
-              m = top;
-            }
-            if (x >= 2 && __any_sync(kFullMask, live && f != 1.f)) {
-              l *= f;
+            if (__any_sync(kFullMask, live && top > reach)) {
+              // the maximum moves (for the first block, or by more than 2^kLazy)
+              float f = 1.f;
+              if (top > reach) {
+                if (m != -INFINITY) f = ex2_approx((m - top) * sc);
+                m = top;
+                off = H::kOffset - m * sc;
+                reach = m + P.lazy;
+                l *= f;
+              }
+              if (x >= 2) {
 #pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[16];
-                tmem_ld16(mO + 16 * q, o);
-                tmem_wait_ld16(o);
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t o[16];
+                  tmem_ld16(mO + 16 * q, o);
+                  tmem_wait_ld16(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(mO + 16 * q, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(mO + 16 * q, o);
+                }
               }
             }
-            const float off = m == -INFINITY ? 0.f : H::kOffset - m * sc;
             const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
             uint64_t sum[2] = {0, 0};
+            // 16 scores at a time, the next 16 on their way
+            uint32_t s[2][16];
+            tmem_ld16(mS + 64 * half, s[0]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t s[32], p[16];
-              tmem_ld32(mS + 64 * half + 32 * q, s);
-              tmem_wait_ld(s);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t(&y)[16] = s[q & 1];
+              tmem_wait_ld16(y);
+              if (q < 3) tmem_ld16(mS + 64 * half + 16 * (q + 1), s[(q + 1) & 1]);
               if (edge) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((seen[q] >> e) & 1)) s[e] = 0xff800000u;
+                for (int e = 0; e < 16; ++e)
+                  if (!((seen[q / 2] >> (16 * (q & 1) + e)) & 1)) y[e] = 0xff800000u;
               }
+              uint32_t p[8];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 y =
-                    unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, off2));
-                const float a = ex2_approx(y.x), d = ex2_approx(y.y);
+              for (int e = 0; e < 8; ++e) {
+                const float2 z =
+                    unpack2(fma2(pack2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), sc2, off2));
+                const float a = ex2_approx(z.x), d = ex2_approx(z.y);
                 sum[e & 1] = add2(sum[e & 1], pack2(a, d));
                 p[e] = H::pack(a, d);
               }
-              tmem_st16(mS + 64 * half + 16 * q, p);
+              tmem_st8(mS + 64 * half + 8 * q, p);
             }
             const float2 t2 = unpack2(add2(sum[0], sum[1]));
             l += t2.x + t2.y;
@@ -1011,11 +1035,12 @@ __global__ void __launch_bounds__(640, 1)
           }
         }
         if (edge) {
+          const int b = rows2 ? x >> 1 : x, k0 = sg.t.kbeg + (sg.blk + b) * kKeyBlock;
           const int t_v = 2 * (kb + b) + 1, st = t_v % R::kStages;
           if (ok) ok = wait_for(&ctl->full[st], (t_v / R::kStages) & 1, ctl, P.wait_ns);
           // (a unit of two row tiles: both streams use the values)
           if (ok)
-            clean_values<T, D>(ring + st * R::kTile, max(ctx - k0, 0), min(kend - k0, kKeyBlock),
+            clean_values<T, D>(ring + st * R::kTile, max(sg.t.ctx - k0, 0), min(sg.t.kend - k0, kKeyBlock),
                                rows2 ? tid : tid & 255, rows2 ? 512 : 256, ctl);
           if (rows2) named_sync(11, 512);
           else named_sync(9 + w, 256);
@@ -1052,10 +1077,11 @@ __global__ void __launch_bounds__(640, 1)
       if (both) l += (ctl->x[wa ^ 1][0][row] + ctl->x[wa ^ 1][1][row]) * f1;
       // a unit of two row tiles: a warpgroup half of its rows' sums; else each
       // of the four a quarter, both streams' sums added up
+      const int nb = sg.nb, kind = sg.t.kind;
+      const int r = row + (rows2 ? 128 * x0 : 0), rr = sg.t.row0 + r, tok = P.rep_div(rr);
       const bool direct = nb == sg.t.blocks && kind == 0;
-      const int head = sg.head, seq_row = sg.t.seq_row;
       const bool bad = ctl->bad && kind != 1;
-      const int64_t q_row = ((int64_t)sg.t.i0 * P.N + tok) * P.q_heads + head * P.rep + rr - tok * P.rep;
+      const int64_t q_row = ((int64_t)sg.t.i0 * P.N + tok) * P.q_heads + sg.head * P.rep + rr - tok * P.rep;
       int64_t slot = 0;
       if (!direct) {
         // a whole unit that is joined with others: the store of its kind; else
@@ -1101,16 +1127,18 @@ __global__ void __launch_bounds__(640, 1)
         __syncwarp();
       }
       if (bad && live)
-        add_unclean<T>(P, seq_row, head, base, lim, see, max(ctx, kseg), min(kend, kseg + nb * kKeyBlock), d0, cols,
+        add_unclean<T>(P, sg.t.seq_row, sg.head, sg.t.base, lim, see,
+                       max(sg.t.ctx, sg.t.kbeg + sg.blk * kKeyBlock),
+                       min(sg.t.kend, sg.t.kbeg + (sg.blk + nb) * kKeyBlock), d0, cols,
                        direct ? P.out + (q_row * D + d0) * 2 : nullptr, P.plan.o + slot * D + d0);
       if (live && !direct && half == 0 && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+      last = sg.last;
       // the exchange and the flag may be used again
       named_sync(12, 512);
       if (bad && tid == 0) ctl->bad = 0;
       g0 += items;
       kb += nb;
       qt += rows2 ? 2 : 1;
-      last = ends;
     }
     if (!ok) {
       // the sequences of this and the following units have no result
@@ -1259,10 +1287,11 @@ int pool_map(const KvView& c, int32_t dtype, void* pool, CUtensorMap* map) {
 }
 
 template <typename T, int D>
-int attend(const AttendParams& P, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   if (cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes) !=
       cudaSuccess)
     return SAMSPEC_ECUDA;
+  P.lazy = Type16<T>::kLazy / P.scale_log2;
   attend_kernel<T, D><<<kKvCtas, 640, Ring<D>::kBytes, s>>>(P, mk, mv);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
   const int per = rows >= kKvCtas * 32 * 8 ? 8 : rows >= kKvCtas * 32 * 2 ? 2 : 1;
