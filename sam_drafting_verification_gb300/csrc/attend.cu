@@ -163,13 +163,13 @@ constexpr int kMinShared = 128;  // tokens: less is read by each sequence for it
 // two row tiles (two steps of softmax on each warp), and what a unit costs
 // besides its blocks (the start and end of its two streams).
 constexpr int kUnitCost = 4;
-__device__ __forceinline__ int block_cost(const KvTile& t) { return t.rows > 128 ? 2 : 1; }
+__device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? 2 : 1; }
 
 __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __shared__ int part[32];
   const KvView& c = P.c;
   const int tid = threadIdx.x, n = P.n;
-  const int rows = P.N * P.rep;  // of one sequence and key head
+  const int tt = tile_tokens(P.rep);
   KvSeq* seq = P.plan.seq;
   if (P.group) {
     for (int i = tid; i < n; i += 1024)
@@ -201,35 +201,33 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
       int cnt = 0;
       if (i < n) {
         if (pass == 0) {
-          if (seq[i].leader == i && seq[i].shared > 0) cnt = (seq[i].gsize * rows + kTileRows - 1) / kTileRows;
+          if (seq[i].leader == i && seq[i].shared > 0) cnt = (seq[i].gsize * P.N + 2 * tt - 1) / (2 * tt);
         } else {
-          cnt = (seq[i].ntok * P.rep + kTileRows - 1) / kTileRows;
+          cnt = (seq[i].ntok + 2 * tt - 1) / (2 * tt);
         }
       }
       int sum;
       const int at = tiles + block_scan(cnt, part, &sum);
       if (i < n) (pass ? P.plan.suf0 : P.plan.pre0)[i] = at;
       for (int k = 0; k < cnt; ++k) {
-        KvTile t;
-        t.i0 = i;
-        t.row0 = k * kTileRows;
-        t.base = seq[i].base;
-        t.ntok = seq[i].ntok;
+        KvTile t = {};
+        const int t0 = 2 * tt * k;
+        t.tok0 = i * P.N + t0;
         t.seq_row = seq[i].row;
         if (pass == 0) {
-          t.rows = min(kTileRows, seq[i].gsize * rows - t.row0);
-          t.kbeg = 0;
+          t.toks = min(2 * tt, seq[i].gsize * P.N - t0);
           t.kend = t.ctx = seq[i].shared;
           t.kind = 1;
         } else {
-          t.rows = min(kTileRows, t.ntok * P.rep - t.row0);
+          t.toks = min(2 * tt, seq[i].ntok - t0);
           t.kbeg = seq[i].shared;
           // a chain's tile sees no further than its last token, and all of it
           // up to its first; a tree's nodes all see the root
-          t.kend = t.base + (P.first_child ? t.ntok : (t.row0 + t.rows - 1) / P.rep + 1);
-          t.ctx = t.base + (P.first_child ? 1 : t.row0 / P.rep + 1);
+          t.kend = seq[i].base + (P.first_child ? seq[i].ntok : t0 + t.toks);
+          t.ctx = seq[i].base + 1 + (P.first_child ? 0 : t0);
           t.kind = t.kbeg > 0 ? 2 : 0;
         }
+        t.two = t.toks > tt;
         t.blocks = (t.kend - t.kbeg + kKeyBlock - 1) / kKeyBlock;
         t.cost0 = 0;
         P.plan.tile[at + k] = t;
@@ -406,6 +404,13 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int x, int y, int z, int u, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
@@ -462,7 +467,7 @@ struct Type16<__half> {
 // Every tile is D / 64 slabs of 128 rows of 128 bytes in the 128-byte swizzle
 // (16-byte piece c of row r lies at piece c ^ (r % 8)), which TMA writes and
 // the matrix instructions read.
-struct Segment {  // what the queries' loader hands on of a segment
+struct Segment {  // what the loader hands on of a segment
   KvTile t;
   int32_t head, blk, nb, last;
 };
@@ -470,7 +475,7 @@ struct Ctl {
   uint64_t full[11], empty[11], s_full[2], p_full[2], q_full[2], q_empty[2], o_done, o_free, drain;
   uint32_t tmem;
   int32_t abort, bad;
-  float x[2][2][128];  // maxima and sums that are exchanged: stream, half of the keys, row
+  float2 ml[2][128];  // running maxima and sums that the streams exchange
   alignas(16) Segment seg[4];
 };
 template <int D>
@@ -537,7 +542,7 @@ struct Walk {
     if (more()) {
       const int4* s = reinterpret_cast<const int4*>(P.plan.tile + tile);
       const int4 a = s[0], b = s[1], c = s[2];
-      t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+      t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
       nb = (tile == end.x && head == end.y ? end.z : t.blocks) - blk;
     }
   }
@@ -655,11 +660,11 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
   }
 }
 
-// One persistent CTA an SM, 20 warps.  Warp 16 loads pages by TMA, warp 17
-// issues matrix products, warps 18 and 19 load queries, two pairs of
-// warpgroups do the softmax: a pair has a stream, each of its two halves of a
-// block's keys, a thread a row of them.  (One warpgroup a stream, a thread all
-// 128 keys of its row, took 2700 clocks a step where the pair takes ...)
+// One persistent CTA an SM.  Warp 8 loads queries and pages by TMA, warp 9
+// issues matrix products, two warpgroups do the softmax, a thread a row.  (What
+// is spilled goes to L2, since shared memory leaves no L1: a thread holds a
+// row's 128 scores in registers.  Two warpgroups a stream of 64 keys each have
+// 104 registers a thread and read the scores twice: ...)
 //
 // A step is one block of 128 keys against 128 query rows: S = Q K^T (both in
 // shared memory, S in tensor memory), P = exp2(S - m) rounded to 16 bits over
@@ -677,9 +682,9 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
 // memory time: at 128 keys * D * 4 bytes a step HBM takes about 2800 clocks an
 // SM, the two products 1024, a warp's softmax about 1500 with two in flight.
 template <typename T, int D>
-__global__ void __launch_bounds__(640, 1)
+__global__ void __launch_bounds__(384, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v) {
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q) {
   using R = Ring<D>;
   using H = Type16<T>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(640, 1)
     if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     return;
   }
-  if (warp == 17) tmem_alloc(&ctl->tmem, 512);
+  if (warp == 9) tmem_alloc(&ctl->tmem, 512);
   if (tid == 0) {
     for (int s = 0; s < R::kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
@@ -700,12 +705,12 @@ __global__ void __launch_bounds__(640, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&ctl->s_full[w], 1);
-      mbar_init(&ctl->p_full[w], 8);
-      mbar_init(&ctl->q_full[w], 2);
-      mbar_init(&ctl->q_empty[w], 2);  // its products are done, its segment has been seen
+      mbar_init(&ctl->p_full[w], 4);
+      mbar_init(&ctl->q_full[w], 1);
+      mbar_init(&ctl->q_empty[w], 1);
     }
     mbar_init(&ctl->o_done, 1);
-    mbar_init(&ctl->o_free, 16);
+    mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     ctl->bad = 0;
@@ -717,17 +722,32 @@ __global__ void __launch_bounds__(640, 1)
   const uint32_t tmem = ctl->tmem;
   const uint32_t tS = tmem, tO = tmem + 256;  // streams 128 columns apart
 
-  // registers: 640 * 96 at launch = 512 * 104 + 128 * 64
-  if (warp >= 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 16) {
-      // ---- pages to the ring ----
-      int kt = 0;  // tiles requested
+  const int tt = tile_tokens(P.rep);
+  // registers: 384 * 168 at launch = 256 * 216 + 128 * 72
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      // ---- queries and pages ----
+      int kt = 0, qt = 0, seg = 0;  // tiles requested, of keys and values and of queries; segments
       bool ok = true;
       constexpr int kSlabs = D / 64;
       const int x = lane / kSlabs, slab = lane % kSlabs;
       const int per = kKeyBlock >> c.log_page;  // pages of a block
-      for (Walk wk(P); ok && wk.more(); wk.next(P)) {
+      for (Walk wk(P); ok && wk.more(); wk.next(P), ++seg) {
+        for (int h = 0; ok && h <= wk.t.two; ++h) {
+          uint64_t* bar = &ctl->q_full[qt & 1];
+          ok = wait_for(&ctl->q_empty[qt & 1], ((qt >> 1) & 1) ^ 1, ctl, P.wait_ns);
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            if (h == 0) ctl->seg[seg & 3] = {wk.t, wk.head, wk.blk, wk.nb, wk.final_one(P)};
+            mbar_arrive_expect_tx(bar, (uint32_t)(tt * P.rep) * D * 2);
+          }
+          __syncwarp();
+          if (lane < kSlabs)
+            tma_load4(smem + (qt & 1) * R::kTile + lane * 16384, &map_q, lane * 64, 0, wk.head, wk.t.tok0 + h * tt, bar);
+          ++qt;
+        }
         const int32_t* table = c.table + (int64_t)wk.t.seq_row * c.max_pages;
         int key0 = wk.t.kbeg + wk.blk * kKeyBlock;
         auto fetch = [&](int k0) {
@@ -756,10 +776,12 @@ __global__ void __launch_bounds__(640, 1)
         }
       }
       // given up: what was requested has to land before the CTA may end
-      if (!ok)
+      if (!ok) {
+        for (int t = qt < 2 ? 0 : qt - 2; t < qt; ++t) drain_wait(&ctl->q_full[t & 1], (t >> 1) & 1);
         for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
           drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
-    } else if (warp == 17) {
+      }
+    } else if (warp == 9) {
       // ---- matrix products ----
       if (lane == 0) {
         const uint32_t id = (1u << 4) | (H::kFormat << 7) | (H::kFormat << 10) | ((128 >> 4) << 24);
@@ -783,8 +805,8 @@ __global__ void __launch_bounds__(640, 1)
           tc_fence_after();
           const uint32_t vl = ring_low + v_stage * (R::kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows; P's halves lie 64 columns apart
-            mma_ts(tO + 128 * w, tS + 128 * w + (k / 4) * 64 + (k % 4) * 8, desc(vl + k * (2048 >> 4)), id_o,
+          for (int k = 0; k < 8; ++k)  // 16 keys: two groups of 8 rows
+            mma_ts(tO + 128 * w, tS + 128 * w + 8 * k, desc(vl + k * (2048 >> 4)), id_o,
                    !(v_what & kFirst) || k > 0);
           if (v_what & kRelease) mma_commit(&ctl->empty[v_stage]);
           if (v_what & kEnd) mma_commit(&ctl->o_done);
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(640, 1)
           ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
           if (!ok) break;
           const int nb = ctl->seg[seg & 3].nb;
-          const bool rows2 = ctl->seg[seg & 3].t.rows > 128;
+          const bool rows2 = ctl->seg[seg & 3].t.two;
           last = ctl->seg[seg & 3].last;
           if (rows2) ok = wait_for(&ctl->q_full[(qt + 1) & 1], ((qt + 1) >> 1) & 1, ctl, P.wait_ns);
           const int items = rows2 ? 2 * nb : nb;
@@ -811,8 +833,6 @@ __global__ void __launch_bounds__(640, 1)
               mma_ss(tS + 128 * w, desc(ql + at), desc(kl + at), id_s, k > 0);
             }
             mma_commit(&ctl->s_full[w]);
-            if (done) mma_commit(&ctl->empty[st]);
-            if (x + 1 >= items - (int)rows2) mma_commit(&ctl->q_empty[(qt + half) & 1]);
             if (v_stage >= 0) product();
             int vs = st + 1, vp = par;
             if (vs == R::kStages) vs = 0, vp ^= 1;
@@ -834,62 +854,16 @@ __global__ void __launch_bounds__(640, 1)
         }
       }
       __syncwarp();
-    } else {
-      // ---- queries ----
-      // Two warps, 64 rows of a tile each, one segment ahead of the products.
-      // A lane finds its rows' addresses; all copies are in flight at once.
-      bool ok = true;
-      int qt = 0, seg = 0;
-      for (Walk wk(P); ok && wk.more(); wk.next(P), ++seg) {
-        const bool rows2 = wk.t.rows > 128;
-        for (int half = 0; half < (rows2 ? 2 : 1); ++half, ++qt) {
-          ok = ok && wait_for(&ctl->q_empty[qt & 1], ((qt >> 1) & 1) ^ 1, ctl, P.wait_ns);
-          ok = __all_sync(kFullMask, ok);
-          if (!ok) break;
-          constexpr int kPer = D / 8;       // copies of a row
-          constexpr int kRows = 32 / kPer;  // rows of one step of the warp
-          unsigned char* dst = smem + (qt & 1) * R::kTile;
-          const int pc = lane % kPer;
-#pragma unroll 1
-          for (int z = 0; z < 2; ++z) {
-            const int r0 = 64 * (warp - 18) + 32 * z, lr = 128 * half + r0 + lane;
-            int64_t mine = -1;
-            if (lr < wk.t.rows) {
-              // (sequences' tokens follow one another)
-              const int rr = wk.t.row0 + lr, tok = P.rep_div(rr);
-              mine = ((int64_t)wk.t.i0 * P.N + tok) * P.q_stride + (int64_t)(wk.head * P.rep + rr - tok * P.rep) * D;
-            }
-#pragma unroll 4
-            for (int y = 0; y < 32; y += kRows) {
-              const int e = y + lane / kPer, rt = r0 + e;
-              const int64_t from = __shfl_sync(kFullMask, mine, e);
-              if (from >= 0)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(dst + (pc >> 3) * 16384 + rt * 128 + (((pc & 7) ^ (rt & 7)) << 4))),
-                             "l"(P.q + from * 2 + pc * 16)
-                             : "memory");
-            }
-          }
-          if (warp == 18 && lane == 0 && half == 0) {
-            ctl->seg[seg & 3] = {wk.t, wk.head, wk.blk, wk.nb, wk.final_one(P)};
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->q_full[qt & 1]);
-        }
-      }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax ----
     // A thread that gives up keeps taking part in every barrier and arrival
     // of its segment, without work, so that no other waits for it.
-    const int w = warp >> 3, half = (warp >> 2) & 1;  // stream, half of the keys
-    const int row = (warp & 3) * 32 + lane;           // its lane of tensor memory
-    const int pair = 1 + w * 4 + (warp & 3);          // barrier with the other half's warp
+    const int w = warp >> 2;                 // stream
+    const int row = (warp & 3) * 32 + lane;  // its lane of tensor memory
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes + half * (D / 2);
+    const uint32_t mS = tS + 128 * w + lanes, mO = tO + 128 * w + lanes;
     const float sc = P.scale_log2;
     const bool tree = P.plan.hdr[kHdrTree] != 0;
     int g0 = 0, kb = 0, qt = 0, seg = 0;  // steps, blocks, query tiles and segments before
@@ -897,16 +871,12 @@ __global__ void __launch_bounds__(640, 1)
     bool ok = true;
     for (; !last; ++seg) {
       ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
-      if (named_any(12, 512, !ok)) {
+      if (named_any(4, 256, !ok)) {
         ok = false;
         break;
       }
       const Segment& sg = ctl->seg[seg & 3];  // the loader is two segments ahead at most
-      if (tid == 0) {
-        mbar_arrive(&ctl->q_empty[qt & 1]);
-        if (sg.t.rows > 128) mbar_arrive(&ctl->q_empty[(qt + 1) & 1]);
-      }
-      const bool rows2 = sg.t.rows > 128;
+      const bool rows2 = sg.t.two;
       const int items = rows2 ? 2 * sg.nb : sg.nb;
       const int x0 = (w - g0) & 1;  // this stream's first step of the segment
       // what the row sees: keys before lim, and a tree's nodes; the first step
@@ -915,124 +885,105 @@ __global__ void __launch_bounds__(640, 1)
       int lim, x_edge;
       uint32_t see = 0;
       {
-        const int r = row + (rows2 ? 128 * x0 : 0), tok = P.rep_div(sg.t.row0 + r);  // this thread's row
-        live = r < sg.t.rows;
-        busy = r - lane < sg.t.rows;
+        const int t0 = rows2 ? tt * x0 : 0, lt = P.rep_div(row);  // this thread's token, of its tile's
+        live = lt < tt && t0 + lt < sg.t.toks;
+        busy = P.rep_div(row - lane) < min(tt, sg.t.toks - t0);
         lim = sg.t.kend;
         if (live && sg.t.kind != 1) {
           if (tree) {
-            see = (uint32_t)P.plan.node[(int64_t)sg.t.i0 * P.N + tok].y;
-            lim = sg.t.base;
+            see = (uint32_t)P.plan.node[sg.t.tok0 + t0 + lt].y;
+            lim = sg.t.ctx - 1;
           } else {
-            lim = min(lim, sg.t.base + tok + 1);
+            lim = min(lim, sg.t.ctx + t0 + lt);
           }
         }
         const int before = sg.t.ctx - sg.t.kbeg - sg.blk * kKeyBlock;
         x_edge = (before > 0 ? before / kKeyBlock : 0) * (rows2 ? 2 : 1);
       }
       // m in units of raw scores, and how far they may go before it moves; the
-      // exponent's constant; l of this half's keys
+      // exponent's constant
       float m = -INFINITY, reach = -INFINITY, off = 0.f, l = 0.f;
       for (int x = x0; x < items; x += 2) {
         const bool edge = x >= x_edge;
         if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
-        if (busy) {
-          // scores are read twice: holding all 64 between the maximum and the
-          // exponentials would take more registers than there are, and what is
-          // spilled goes to L2 (shared memory leaves no L1)
-          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
-          float top = -INFINITY;
-          if (ok) {
-            if (edge) {
+        if (row == 0) {
+          // the product is done with the block's keys, the last one with the
+          // queries (arrivals here, since each commit of the products' warp
+          // takes the matrix unit 57 clocks)
+          const int t_k = 2 * (kb + (rows2 ? x >> 1 : x));
+          if (!rows2 || (x & 1)) mbar_arrive(&ctl->empty[t_k % R::kStages]);
+          if (x + 1 >= items - (int)rows2) mbar_arrive(&ctl->q_empty[(qt + (rows2 ? x & 1 : 0)) & 1]);
+        }
+        if (ok && busy) {
+          uint32_t s[128];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int ks = sg.t.kbeg + (sg.blk + (rows2 ? x >> 1 : x)) * kKeyBlock + 64 * half + 32 * q;
-                // bits of the 32 keys from ks on: those before lim, and a tree's
-                uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
-                if (see) {
-                  const int d = sg.t.base - ks;
-                  bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
-                }
-                seen[q] = bits;
-              }
-            }
-            uint32_t s[2][16];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            tmem_ld16(mS + 64 * half, s[0]);
+          for (int q = 0; q < 4; ++q) tmem_ld32(mS + 32 * q, s + 32 * q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_wait_ld(s + 32 * q);
+          if (edge) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint32_t(&y)[16] = s[q & 1];
-              tmem_wait_ld16(y);
-              if (q < 3) tmem_ld16(mS + 64 * half + 16 * (q + 1), s[(q + 1) & 1]);
-              if (edge) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((seen[q / 2] >> (16 * (q & 1) + e)) & 1)) y[e] = 0xff800000u;
+              const int ks = sg.t.kbeg + (sg.blk + (rows2 ? x >> 1 : x)) * kKeyBlock + 32 * q;
+              // bits of the 32 keys from ks on: those before lim, and a tree's
+              uint32_t bits = lim - ks >= 32 ? 0xffffffffu : lim > ks ? (1u << (lim - ks)) - 1 : 0;
+              if (see) {
+                const int d = sg.t.ctx - 1 - ks;
+                bits |= d >= 0 ? (d < 32 ? see << d : 0) : (d > -32 ? see >> -d : 0);
               }
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                mx[e & 3] = max3(mx[e & 3], __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1)) s[32 * q + e] = 0xff800000u;
             }
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-            ctl->x[w][half][row] = top;
           }
-          named_sync(pair, 64);
-          if (ok) {
-            top = fmaxf(top, ctl->x[w][half ^ 1][row]);
-            if (__any_sync(kFullMask, live && top > reach)) {
-              // the maximum moves (for the first block, or by more than 2^kLazy)
-              float f = 1.f;
-              if (top > reach) {
-                if (m != -INFINITY) f = ex2_approx((m - top) * sc);
-                m = top;
-                off = H::kOffset - m * sc;
-                reach = m + P.lazy;
-                l *= f;
-              }
-              if (x >= 2) {
+          float mx[4];
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                  uint32_t o[16];
-                  tmem_ld16(mO + 16 * q, o);
-                  tmem_wait_ld16(o);
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(mO + 16 * q, o);
-                }
+          for (int e = 4; e < 64; ++e)
+            mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          if (__any_sync(kFullMask, live && top > reach)) {
+            // the maximum moves (for the first block, or by more than 2^kLazy)
+            float f = 1.f;
+            if (top > reach) {
+              if (m != -INFINITY) f = ex2_approx((m - top) * sc);
+              m = top;
+              off = H::kOffset - m * sc;
+              reach = m + P.lazy;
+              l *= f;
+            }
+            if (x >= 2) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(mO + 16 * q, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(mO + 16 * q, o);
               }
             }
-            const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
-            uint64_t sum[2] = {0, 0};
-            // 16 scores at a time, the next 16 on their way
-            uint32_t s[2][16];
-            tmem_ld16(mS + 64 * half, s[0]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t(&y)[16] = s[q & 1];
-              tmem_wait_ld16(y);
-              if (q < 3) tmem_ld16(mS + 64 * half + 16 * (q + 1), s[(q + 1) & 1]);
-              if (edge) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((seen[q / 2] >> (16 * (q & 1) + e)) & 1)) y[e] = 0xff800000u;
-              }
-              uint32_t p[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 z =
-                    unpack2(fma2(pack2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), sc2, off2));
-                const float a = ex2_approx(z.x), d = ex2_approx(z.y);
-                sum[e & 1] = add2(sum[e & 1], pack2(a, d));
-                p[e] = H::pack(a, d);
-              }
-              tmem_st8(mS + 64 * half + 8 * q, p);
-            }
-            const float2 t2 = unpack2(add2(sum[0], sum[1]));
-            l += t2.x + t2.y;
-            tmem_wait_st();
           }
+          const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 z = unpack2(fma2(
+                  pack2(__uint_as_float(s[16 * q + 2 * e]), __uint_as_float(s[16 * q + 2 * e + 1])), sc2, off2));
+              const float a = ex2_approx(z.x), d = ex2_approx(z.y);
+              sum[e & 1] = add2(sum[e & 1], pack2(a, d));
+              p[e] = H::pack(a, d);
+            }
+            tmem_st8(mS + 8 * q, p);
+          }
+          const float2 t2 = unpack2(add2(sum[0], sum[1]));
+          l += t2.x + t2.y;
+          tmem_wait_st();
         }
         if (edge) {
           const int b = rows2 ? x >> 1 : x, k0 = sg.t.kbeg + (sg.blk + b) * kKeyBlock;
@@ -1041,56 +992,52 @@ __global__ void __launch_bounds__(640, 1)
           // (a unit of two row tiles: both streams use the values)
           if (ok)
             clean_values<T, D>(ring + st * R::kTile, max(sg.t.ctx - k0, 0), min(sg.t.kend - k0, kKeyBlock),
-                               rows2 ? tid : tid & 255, rows2 ? 512 : 256, ctl);
-          if (rows2) named_sync(11, 512);
-          else named_sync(9 + w, 256);
+                               rows2 ? tid : row, rows2 ? 256 : 128, ctl);
+          if (rows2) named_sync(3, 256);
+          else named_sync(1 + w, 128);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_full[w]);
       }
       if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
-      // the streams' maxima, then the halves' sums; all threads decide alike
-      // whether to go on
+      // (the streams' maxima and sums); all threads decide alike whether to go on
       const bool both = !rows2 && items > 1;
-      ctl->x[w][half][row] = m;
-      ok = !named_any(12, 512, !ok);
+      ctl->ml[w][row] = {m, l};
+      ok = !named_any(4, 256, !ok);
       if (!ok) break;
       tc_fence_after();
       const int wa = rows2 ? w : g0 & 1;  // the stream of the row's first step
       float f0 = 1.f, f1 = 0.f;
       if (!rows2) {
-        const float ma = ctl->x[wa][0][row];
-        m = ma;
+        const float2 a = ctl->ml[wa][row];
+        m = a.x;
+        l = a.y;
         if (both) {
-          const float mb = ctl->x[wa ^ 1][0][row];
-          m = fmaxf(ma, mb);
+          const float2 z = ctl->ml[wa ^ 1][row];
+          m = fmaxf(a.x, z.x);
           const float mm = m == -INFINITY ? 0.f : m;
-          f0 = ex2_approx((ma - mm) * sc);
-          f1 = ex2_approx((mb - mm) * sc);
+          f0 = ex2_approx((a.x - mm) * sc);
+          f1 = ex2_approx((z.x - mm) * sc);
+          l = a.y * f0 + z.y * f1;
         }
       }
-      named_sync(12, 512);
-      ctl->x[w][half][row] = l;
-      named_sync(12, 512);
-      l = (ctl->x[wa][0][row] + ctl->x[wa][1][row]) * f0;
-      if (both) l += (ctl->x[wa ^ 1][0][row] + ctl->x[wa ^ 1][1][row]) * f1;
-      // a unit of two row tiles: a warpgroup half of its rows' sums; else each
-      // of the four a quarter, both streams' sums added up
+      // a unit of two row tiles: a warpgroup its rows' sums; else each half of
+      // them, both streams' added up
       const int nb = sg.nb, kind = sg.t.kind;
-      const int r = row + (rows2 ? 128 * x0 : 0), rr = sg.t.row0 + r, tok = P.rep_div(rr);
+      const int lt = P.rep_div(row);
       const bool direct = nb == sg.t.blocks && kind == 0;
       const bool bad = ctl->bad && kind != 1;
-      const int64_t q_row = ((int64_t)sg.t.i0 * P.N + tok) * P.q_heads + sg.head * P.rep + rr - tok * P.rep;
+      const int64_t q_row = ((int64_t)sg.t.tok0 + (rows2 ? tt * x0 : 0) + lt) * P.q_heads + sg.head * P.rep + row - lt * P.rep;
       int64_t slot = 0;
       if (!direct) {
         // a whole unit that is joined with others: the store of its kind; else
         // the first segment of a CTA's share, or its last
         slot = nb == sg.t.blocks ? 2 * kKvCtas * kTileRows + (kind == 1 ? P.plan.store : 0) + q_row
-                                 : (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + r;
+                                 : (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + (rows2 ? kRows * x0 : 0) + row;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const int cols = rows2 ? D / 2 : D / 4, d0 = rows2 ? half * (D / 2) : (2 * w + half) * (D / 4);
+      const int cols = rows2 ? D : D / 2, d0 = rows2 ? 0 : w * (D / 2);
       const uint32_t a0 = tO + lanes + 128 * wa + d0, a1 = tO + lanes + 128 * (wa ^ 1) + d0;
 #pragma unroll 1
       for (int d = 0; d < cols; d += 16) {
@@ -1127,14 +1074,14 @@ __global__ void __launch_bounds__(640, 1)
         __syncwarp();
       }
       if (bad && live)
-        add_unclean<T>(P, sg.t.seq_row, sg.head, sg.t.base, lim, see,
+        add_unclean<T>(P, sg.t.seq_row, sg.head, sg.t.ctx - 1, lim, see,
                        max(sg.t.ctx, sg.t.kbeg + sg.blk * kKeyBlock),
                        min(sg.t.kend, sg.t.kbeg + (sg.blk + nb) * kKeyBlock), d0, cols,
                        direct ? P.out + (q_row * D + d0) * 2 : nullptr, P.plan.o + slot * D + d0);
-      if (live && !direct && half == 0 && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
+      if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
       last = sg.last;
       // the exchange and the flag may be used again
-      named_sync(12, 512);
+      named_sync(4, 256);
       if (bad && tid == 0) ctl->bad = 0;
       g0 += items;
       kb += nb;
@@ -1145,8 +1092,8 @@ __global__ void __launch_bounds__(640, 1)
       int k = 0;
       for (Walk wk(P); wk.more(); wk.next(P), ++k)
         if (k >= seg) {
-          const int end = wk.t.i0 + (wk.t.row0 + wk.t.rows - 1) / (P.N * P.rep);
-          for (int j = wk.t.i0 + tid; j <= end; j += 512) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
+          const int end = (wk.t.tok0 + wk.t.toks - 1) / P.N;
+          for (int j = wk.t.tok0 / P.N + tid; j <= end; j += 256) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
         }
       if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     }
@@ -1154,7 +1101,7 @@ __global__ void __launch_bounds__(640, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_free(tmem, 512);
+  if (warp == 9) tmem_free(tmem, 512);
 }
 
 // Rows of units that were cut among CTAs, or that have a shared part: their
@@ -1186,13 +1133,14 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
     if (node >= s.ntok) {
       parts = 0;
     } else {
-      const int h = hq / P.rep, x = node * P.rep + hq % P.rep;
+      const int h = hq / P.rep, tt = tile_tokens(P.rep);
       const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         if (p == 0 && s.shared == 0) continue;
-        const int at = p ? x : (i - s.leader) * P.N * P.rep + x;
-        const int ti = (p ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + at / kTileRows;
+        const int ft = p ? node : (i - s.leader) * P.N + node, lt = ft % (2 * tt);
+        const int at = lt / tt * kRows + lt % tt * P.rep + hq % P.rep;  // its row of the unit
+        const int ti = (p ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + ft / (2 * tt);
         const KvTile t = P.plan.tile[ti];
         const int bc = block_cost(t);
         const int b0 = t.cost0 + h * (t.blocks * bc + kUnitCost);  // the unit's costs begin
@@ -1208,8 +1156,8 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
           // the first segment of a CTA's share, or its last
           const int4 st = P.plan.start[c0];
           const bool begins = st.x == ti && st.y == h && st.z == 0;
-          first[p] = (2 * c0 + !begins) * kTileRows + at % kTileRows;
-          rest[p] = 2 * (c0 + 1) * kTileRows + at % kTileRows;
+          first[p] = (2 * c0 + !begins) * kTileRows + at;
+          rest[p] = 2 * (c0 + 1) * kTileRows + at;
         }
       }
       parts = cnt[0] + cnt[1];
@@ -1286,13 +1234,30 @@ int pool_map(const KvView& c, int32_t dtype, void* pool, CUtensorMap* map) {
              : SAMSPEC_ECUDA;
 }
 
+// queries as [tokens][kv_heads][rep][head_dim], in boxes of one tile's tokens
+// of one key head, 64 elements wide
+int query_map(const AttendParams& P, int32_t dtype, CUtensorMap* map) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return SAMSPEC_ECUDA;
+  const cuuint64_t D = P.c.head_dim, rep = P.rep;
+  const cuuint64_t dims[4] = {D, rep, (cuuint64_t)P.c.kv_heads, (cuuint64_t)P.n * P.N};
+  const cuuint64_t strides[3] = {D * 2, rep * D * 2, (cuuint64_t)P.q_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rep, 1, (cuuint32_t)tile_tokens(P.rep)}, one[4] = {1, 1, 1, 1};
+  return enc(map, dtype == SAMSPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<unsigned char*>(P.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SAMSPEC_OK
+             : SAMSPEC_ECUDA;
+}
+
 template <typename T, int D>
-int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t s) {
   if (cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes) !=
       cudaSuccess)
     return SAMSPEC_ECUDA;
   P.lazy = Type16<T>::kLazy / P.scale_log2;
-  attend_kernel<T, D><<<kKvCtas, 640, Ring<D>::kBytes, s>>>(P, mk, mv);
+  attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv, mq);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
   const int per = rows >= kKvCtas * 32 * 8 ? 8 : rows >= kKvCtas * 32 * 2 ? 2 : 1;
   join_kernel<T, D><<<(unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s>>>(P, per);
@@ -1374,13 +1339,14 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   P.scale_log2 = scale * 1.4426950408889634f;
   P.out = static_cast<unsigned char*>(d_out);
   P.wait_ns = g_kv_wait_ns.load();
-  CUtensorMap mk, mv;
-  if (pool_map(P.c, cache->dtype, cache->k, &mk) != SAMSPEC_OK || pool_map(P.c, cache->dtype, cache->v, &mv) != SAMSPEC_OK)
+  CUtensorMap mk, mv, mq;
+  if (pool_map(P.c, cache->dtype, cache->k, &mk) != SAMSPEC_OK || pool_map(P.c, cache->dtype, cache->v, &mv) != SAMSPEC_OK ||
+      query_map(P, cache->dtype, &mq) != SAMSPEC_OK)
     return SAMSPEC_ECUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->dtype == SAMSPEC_BF16)
-    return cache->head_dim == 64 ? attend<__nv_bfloat16, 64>(P, mk, mv, s) : attend<__nv_bfloat16, 128>(P, mk, mv, s);
-  return cache->head_dim == 64 ? attend<__half, 64>(P, mk, mv, s) : attend<__half, 128>(P, mk, mv, s);
+    return cache->head_dim == 64 ? attend<__nv_bfloat16, 64>(P, mk, mv, mq, s) : attend<__nv_bfloat16, 128>(P, mk, mv, mq, s);
+  return cache->head_dim == 64 ? attend<__half, 64>(P, mk, mv, mq, s) : attend<__half, 128>(P, mk, mv, mq, s);
 }
 
 uint64_t kv_set_wait_limit_ns(uint64_t ns) {

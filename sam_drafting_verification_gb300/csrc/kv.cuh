@@ -14,7 +14,8 @@
 namespace samspec {
 
 constexpr int kKvCtas = 152;   // persistent CTAs of kv_attend: one per SM of a GB300
-constexpr int kTileRows = 256; // query rows of a unit of attention work (two MMA tiles)
+constexpr int kRows = 128;     // query rows of a tile (a matrix instruction's)
+constexpr int kTileRows = 256; // of a unit of attention work
 constexpr int kKeyBlock = 128; // keys of one step of it
 
 struct KvView {
@@ -96,20 +97,23 @@ struct KvSeq {
   int32_t gsize;   // the group's sequences (at the leader)
   int32_t pad;
 };
-// a unit of attention work, once for each key head: rows of queries against a
-// range of keys.  Row x is query (x + row0) of sequence i0 on, counted (token,
-// query head within the key head's group), N * rep of them per sequence.
+// a unit of attention work, once for each key head: the queries of `toks`
+// tokens (tokens of consecutive sequences follow one another, rep query heads
+// each) against a range of keys.  Up to kRows / rep tokens make one tile of
+// query rows, up to twice as many a unit of two.
 struct KvTile {
-  int32_t i0, row0, rows;
-  int32_t kbeg, kend;  // tokens
-  int32_t ctx;         // every row sees the keys before this one
-  int32_t base, ntok;  // of the sequence (own keys)
+  int32_t tok0, toks;  // first token of the call (i * N + node), how many
+  int32_t two;         // two tiles of rows
+  int32_t kbeg, kend;  // keys, in tokens
+  int32_t ctx;         // every row sees the keys before this one; token t of a chain those before ctx + t
   int32_t seq_row;     // the cache row whose pages are read
   int32_t kind;        // 1: keys that the group shares, every row sees them all;
                        // 2: own keys of a sequence whose group shares others
   int32_t blocks;      // key blocks
   int32_t cost0;       // cost of all heads of the tiles before
+  int32_t pad[2];
 };
+inline __host__ __device__ int tile_tokens(int rep) { return kRows / rep; }
 enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4, kHdrInts = 16 };
 
 struct PlanLayout {
@@ -128,8 +132,9 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
       q_heads / c.kv_heads > 64 || (int64_t)n * N * q_heads >= ((int64_t)1 << 30))
     return p;
   const int64_t rep = q_heads / c.kv_heads;
-  const int64_t suf = (N * rep + kTileRows - 1) / kTileRows * n;
-  const int64_t pre = grouped ? ((int64_t)n * N * rep + kTileRows - 1) / kTileRows + n : 0;
+  const int64_t unit = 2 * tile_tokens((int)rep);  // tokens
+  const int64_t suf = (N + unit - 1) / unit * n;
+  const int64_t pre = grouped ? ((int64_t)n * N + unit - 1) / unit + n : 0;
   // costs are counted in 32 bits
   const int64_t blocks = ((int64_t)c.max_pages * c.page / kKeyBlock + 2) * 2 + 4;
   if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
