@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
   const KvView& c = P.c;
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  wait_for_previous();
+  let_next_start();
   if (i >= P.n) return;
   int st = SAMSPEC_ST_OK;
   const int row = P.rows ? P.rows[i] : i;
@@ -169,6 +171,8 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __shared__ int part[32];
   const KvView& c = P.c;
   const int tid = threadIdx.x, n = P.n;
+  wait_for_previous();
+  let_next_start();
   const int tt = tile_tokens(P.rep);
   KvSeq* seq = P.plan.seq;
   if (P.group) {
@@ -275,6 +279,8 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
     }
     P.plan.start[x] = s;
   }
+  // CTAs without a share begin where the last one ends
+  for (int x = ctas + 1 + tid; x <= kKvCtas; x += 1024) P.plan.start[x] = {tiles, 0, 0, 0};
   if (tid == 0) {
     P.plan.hdr[kHdrTiles] = tiles;
     P.plan.hdr[kHdrCtas] = ctas;
@@ -692,7 +698,6 @@ __global__ void __launch_bounds__(384, 1)
   unsigned char* ring = smem + 2 * R::kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const KvView& c = P.c;
-  if ((int)blockIdx.x >= P.plan.hdr[kHdrCtas]) return;  // before anything is set up
   if (smem_u32(smem) & 1023) {  // the swizzle counts from there; the linker sees to it
     if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     return;
@@ -717,9 +722,12 @@ __global__ void __launch_bounds__(384, 1)
     mbar_fence_init();
   }
   tc_fence_before();
+  wait_for_previous();
+  let_next_start();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  // (a CTA without a share finds its first segment at its end)
   const uint32_t tS = tmem, tO = tmem + 256;  // streams 128 columns apart
 
   const int tt = tile_tokens(P.rep);
@@ -1110,6 +1118,10 @@ __global__ void __launch_bounds__(384, 1)
 // finds where one row's parts lie, then the warp adds up one row after the
 // other, the loads of up to 4 parts in flight at once.  (Calls of few rows
 // give a warp fewer.)
+#ifndef KJR
+#define KJR 8
+#endif
+constexpr int kJoinRows = KJR;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows) {
   using H = Type16<T>;
@@ -1120,6 +1132,8 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
   const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * warp_rows;
+  wait_for_previous();
+  let_next_start();
   if (r0 >= rows) return;
   // of lane's row: parts (-1: none to join, 0: zeros), and for the shared and
   // the own keys where the first part lies and where the others begin
@@ -1257,10 +1271,11 @@ int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, const C
       cudaSuccess)
     return SAMSPEC_ECUDA;
   P.lazy = Type16<T>::kLazy / P.scale_log2;
-  attend_kernel<T, D><<<kKvCtas, 384, Ring<D>::kBytes, s>>>(P, mk, mv, mq);
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  const int per = rows >= kKvCtas * 32 * 8 ? 8 : rows >= kKvCtas * 32 * 2 ? 2 : 1;
-  join_kernel<T, D><<<(unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s>>>(P, per);
+  const int per = rows >= kKvCtas * 32 * 8 ? kJoinRows : rows >= kKvCtas * 32 * 2 ? 2 : 1;
+  if (launch_after(attend_kernel<T, D>, kKvCtas, 384, Ring<D>::kBytes, s, P, mk, mv, mq) != cudaSuccess ||
+      launch_after(join_kernel<T, D>, (unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s, P, per) != cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 
@@ -1308,8 +1323,9 @@ int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, 
   P.q_heads = q_heads;
   P.rep = q_heads / P.c.kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  plan_sequences_kernel<<<(n + 7) / 8, 256, 0, s>>>(P);
-  plan_units_kernel<<<1, 1024, 0, s>>>(P);
+  if (launch_after(plan_sequences_kernel, (n + 7) / 8, 256, 0, s, P) != cudaSuccess ||
+      launch_after(plan_units_kernel, 1, 1024, 0, s, P) != cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 

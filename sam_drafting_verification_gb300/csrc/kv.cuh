@@ -83,6 +83,25 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   return before + s - v;
 }
 
+// Programmatic dependent launch: a kernel may be started while the one before
+// it in the stream still runs; nothing that one writes, or may still read, is
+// touched before wait_for_previous().  (Launch gaps of about 2 us a kernel.)
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, B... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, A(args)...);
+}
 inline int launched() { return cudaGetLastError() == cudaSuccess ? SAMSPEC_OK : SAMSPEC_ECUDA; }
 
 // ---- plan ------------------------------------------------------------------
