@@ -49,6 +49,12 @@ def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(index):
+    """torch's current stream of a CUDA device as an integer (without building
+    the stream object, which takes longer than the rest of a call's checks)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _is_cuda(t):
     return t.is_cuda
 

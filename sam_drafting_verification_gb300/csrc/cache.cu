@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(1024) reserve_kernel(KvView c, const int32_t* 
                                                        int32_t* __restrict__ status, ReserveWs w) {
   __shared__ int part[32];
   const int tid = threadIdx.x;
+  wait_for_previous();
+  let_next_start();
   for (int i = tid; i < n; i += 1024) {
     const int row = rows ? rows[i] : i;
     if (row >= 0 && row < c.seqs) w.claim[row] = 0x7fffffff;
@@ -164,6 +166,8 @@ __global__ void __launch_bounds__(1024) reserve_kernel(KvView c, const int32_t* 
 __global__ void __launch_bounds__(256) copy_pages_kernel(KvView c, const int32_t* __restrict__ cow) {
   const int lane = threadIdx.x & 31;
   const int64_t per = (int64_t)c.layers * 2 * c.kv_heads;
+  wait_for_previous();
+  let_next_start();
   const int64_t items = cow[0] * per;
   const int64_t warps = (int64_t)gridDim.x * 8;
   for (int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); x < items; x += warps) {
@@ -194,6 +198,8 @@ __global__ void __launch_bounds__(256) fork_kernel(KvView c, const int32_t* __re
                                                    const int32_t* __restrict__ dst, int n,
                                                    int32_t* __restrict__ status) {
   const int i = blockIdx.x, tid = threadIdx.x;
+  wait_for_previous();
+  let_next_start();
   const int s = src[i], d = dst[i];
   int st = SAMSPEC_ST_OK;
   if (s < 0 || s >= c.seqs || d < 0 || d >= c.seqs) st = SAMSPEC_ST_ROW;
@@ -255,6 +261,7 @@ __device__ __forceinline__ Judged judge(const KvView& c, const int32_t* __restri
   Judged j = {SAMSPEC_ST_OK, rows ? rows[i] : i, 0, 0, 0, 0, -1};
   bool twice = false;
   if (rows)
+#pragma unroll 8
     for (int k = lane; k < n; k += 32) twice |= k != i && rows[k] == j.row;
   if (__any_sync(kFullMask, twice) || j.row < 0 || j.row >= c.seqs) {
     j.st = SAMSPEC_ST_ROW;
@@ -309,10 +316,13 @@ __device__ __forceinline__ Judged judge(const KvView& c, const int32_t* __restri
   return j;
 }
 
-// Accepted nodes' keys and values to the front of their slots: a warp takes
-// one (sequence, layer, pool, head).  Targets may be sources of nodes before
-// them, so a warp reads all of its rows into registers before it writes; no
-// other warp touches them.
+// Accepted nodes' keys and values to the front of their slots.  A CTA takes
+// one sequence and 64 of its (layer, pool, head), judges it once (the judging
+// is a chain of a dozen reads, as long as all the moves), and gives its warps
+// one after the other.  Targets may be sources of nodes before them, so a warp
+// reads all of its rows into registers before it writes; no other warp touches
+// them.
+constexpr int kMoveItems = 64;
 template <int D>
 __global__ void __launch_bounds__(256) move_path_kernel(KvView c, const int32_t* __restrict__ rows,
                                                         int n, int N,
@@ -322,44 +332,50 @@ __global__ void __launch_bounds__(256) move_path_kernel(KvView c, const int32_t*
   constexpr int kLanes = D / 8;           // 16-byte pieces of a row
   constexpr int kRows = 32 / kLanes;      // rows at a time
   constexpr int kSteps = 32 / kRows;      // 31 rows at most
-  const int lane = threadIdx.x & 31;
-  const int64_t per = (int64_t)c.layers * 2 * c.kv_heads;
-  const int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (x >= n * per) return;
-  const int i = (int)(x / per);
-  int r = (int)(x % per);
-  const int head = r % c.kv_heads;
-  r /= c.kv_heads;
-  unsigned char* pool = r & 1 ? c.v : c.k;
-  const int layer = r >> 1;
-  const Judged j = judge(c, rows, n, i, N, accept, path, nullptr, lane);
-  if (lane == 0 && x % per == 0) status[i] = j.st;  // set_len_kernel goes by it
-  if (j.st != SAMSPEC_ST_OK || j.accept < 1) return;
-  const bool stays = lane >= j.accept || j.path == lane + 1;
-  if (__all_sync(kFullMask, stays)) return;
-  const int32_t* t = c.table + (int64_t)j.row * c.max_pages;
-  const int col = lane % kLanes;
-  uint4 buf[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int e = s * kRows + lane / kLanes;
-    const int node = __shfl_sync(kFullMask, j.path, e & 31);
-    if (e < j.accept) {
-      const int slot = j.len + node, p = t[slot >> c.log_page];
-      if (p >= 0 && p < c.n_pages)
-        buf[s] = reinterpret_cast<const uint4*>(pool + kv_offset(c, layer, p, head))[(slot & (c.page - 1)) *
-                                                                                   kLanes + col];
+  __shared__ int accepted;
+  __shared__ int64_t from[32], to[32];    // bytes from (layer, head) 0 of a pool
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int items = c.layers * 2 * c.kv_heads;
+  const int parts = (items + kMoveItems - 1) / kMoveItems;
+  const int i = blockIdx.x / parts, part = blockIdx.x % parts;
+  wait_for_previous();
+  let_next_start();
+  if (warp == 0) {
+    const Judged j = judge(c, rows, n, i, N, accept, path, nullptr, lane);
+    if (lane == 0 && part == 0) status[i] = j.st;  // set_len_kernel goes by it
+    const bool moves = lane < j.accept && j.path != lane + 1;
+    const bool any = __any_sync(kFullMask, moves);
+    int a = j.st == SAMSPEC_ST_OK && any ? j.accept : 0;
+    bool bad = false;
+    if (lane < a) {
+      const int32_t* t = c.table + (int64_t)j.row * c.max_pages;
+      const int s = j.len + j.path, d = j.len + 1 + lane;
+      const int ps = t[s >> c.log_page], pd = t[d >> c.log_page];
+      bad = ps < 0 || ps >= c.n_pages || pd < 0 || pd >= c.n_pages;
+      from[lane] = kv_offset(c, 0, ps, 0) + (int64_t)(s & (c.page - 1)) * D * 2;
+      to[lane] = kv_offset(c, 0, pd, 0) + (int64_t)(d & (c.page - 1)) * D * 2;
     }
+    if (__any_sync(kFullMask, bad)) a = 0;
+    if (lane == 0) accepted = a;
   }
-  __syncwarp();
+  __syncthreads();
+  const int a = accepted;
+  if (a == 0) return;
+  const int col = lane % kLanes * 16;
+  for (int x = part * kMoveItems + warp; x < min(items, (part + 1) * kMoveItems); x += 8) {
+    const int head = x % c.kv_heads, r = x / c.kv_heads;
+    unsigned char* pool = (r & 1 ? c.v : c.k) + kv_offset(c, r >> 1, 0, head) + col;
+    uint4 buf[kSteps];
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int e = s * kRows + lane / kLanes;
-    if (e < j.accept) {
-      const int slot = j.len + 1 + e, p = t[slot >> c.log_page];
-      if (p >= 0 && p < c.n_pages)
-        reinterpret_cast<uint4*>(pool + kv_offset(c, layer, p, head))[(slot & (c.page - 1)) * kLanes + col] =
-            buf[s];
+    for (int s = 0; s < kSteps; ++s) {
+      const int e = s * kRows + lane / kLanes;
+      if (e < a) buf[s] = *reinterpret_cast<const uint4*>(pool + from[e]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int e = s * kRows + lane / kLanes;
+      if (e < a) *reinterpret_cast<uint4*>(pool + to[e]) = buf[s];
     }
   }
 }
@@ -373,6 +389,8 @@ __global__ void __launch_bounds__(256) set_len_kernel(KvView c, const int32_t* _
                                                       int32_t* __restrict__ status) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  wait_for_previous();
+  let_next_start();
   if (i >= n) return;
   Judged j = judge(c, rows, n, i, N, accept, nullptr, new_len, lane);
   if (path) j.st = status[i];
@@ -402,7 +420,7 @@ __global__ void __launch_bounds__(256) set_len_kernel(KvView c, const int32_t* _
 struct AppendParams {
   KvView c;
   PlanView plan;
-  int layer, n, N, q_heads, rot, interleaved;
+  int layer, n, N, q_heads, rot, parts;
   const unsigned char* q;
   unsigned char* q_out;
   const unsigned char* k;
@@ -441,121 +459,143 @@ __device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
 // position * 2^-53 turns whatever the position.  Its top bits go to fp32 half
 // turns in [-1, 1) for sincospif.
 //
-// One CTA a token at a time: sines and cosines once for all heads, then the
-// heads in 16-byte vectors.  Reads q, k, v and writes q', K, V once; bound by
+// A warp takes a token (for few tokens, a part of its heads): its sines and
+// cosines, then its heads, eight 16-byte loads of a lane in flight.  A lane's
+// place in a head is the same for all of them, and so are its sines and
+// cosines; in the half layout the other elements of its pairs come from the
+// lane that has loaded them.  Reads q, k, v and writes q', K, V once: bound by
 // HBM for prompts, by latency for a decode step.
-template <typename T>
-__global__ void __launch_bounds__(256) append_kernel(AppendParams P) {
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(256, 2) append_kernel(AppendParams P) {
+  constexpr int kVec = D / 8, kStep = 32 / kVec;  // vectors of a head, heads at a time
+  constexpr int kDeep = 8;
   __shared__ uint64_t turn[64];
-  __shared__ float2 cs[64];
+  __shared__ float2 cs[8][64];  // each warp's cosines and sines
   const KvView& c = P.c;
-  const int tid = threadIdx.x, D = c.head_dim, half = P.rot / 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = P.rot / 2;
+  wait_for_previous();
+  let_next_start();
   for (int j = tid; j < half; j += 256) {
     double f = P.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
     f -= floor(f);
     turn[j] = (uint64_t)(f * 18446744073709551616.0);
   }
-  const int vec = D / 8;
+  __syncthreads();
   const bool tree = P.plan.hdr[kHdrTree] != 0;
-  const int heads = (P.q ? P.q_heads : 0) + 2 * c.kv_heads;
+  const int head_bytes = c.page * D * 2;
   const int q_heads = P.q ? P.q_heads : 0;
-  for (int64_t tok = blockIdx.x; tok < (int64_t)P.n * P.N; tok += gridDim.x) {
-    const int i = (int)(tok / P.N), node = (int)(tok % P.N);
-    const KvSeq s = P.plan.seq[i];
-    const bool live = node < s.ntok;
-    __syncthreads();  // turn is written; cs of the last token is read
-    if (live && tid < half) {
-      const int64_t pos = (int64_t)s.base + (tree ? P.plan.node[tok].x : node);
-      const uint64_t a = (uint64_t)pos * turn[tid];
-      float sn, cn;
-      sincospif((float)(int64_t)a * 1.0842021724855044e-19f, &sn, &cn);  // 2^-63
-      cs[tid] = {cn * P.mscale, sn * P.mscale};
-    }
-    __syncthreads();
-    if (!live) {
-      if (P.q)
-        for (int x = tid; x < P.q_heads * vec; x += 256)
-          reinterpret_cast<uint4*>(P.q_out + tok * P.q_heads * D * 2)[x] = uint4{0, 0, 0, 0};
+  const bool vectors = kInterleaved || half % 8 == 0;
+  // this lane's vector: the first of its pairs, and in the half layout whether
+  // it holds their lower (1) or upper (2) elements, and who the others
+  const int e = lane % kVec;
+  int first = 0, role = 0, other = lane;
+  if (kInterleaved) {
+    first = 4 * e;
+    role = 8 * e < P.rot;
+  } else if (e < half / 8) {
+    first = 8 * e;
+    role = 1;
+    other = lane + half / 8;
+  } else if (e < half / 4) {
+    first = 8 * e - half;
+    role = 2;
+    other = lane - half / 8;
+  }
+
+  const int items = P.n * P.N * P.parts;
+#pragma unroll 1
+  for (int item = blockIdx.x * 8 + warp; item < items; item += gridDim.x * 8) {
+    const int tok = item / P.parts, part = item % P.parts, i = tok / P.N, node = tok % P.N;
+    const int q0 = q_heads * part / P.parts, q1 = q_heads * (part + 1) / P.parts;
+    const int k0 = c.kv_heads * part / P.parts, k1 = c.kv_heads * (part + 1) / P.parts;
+    const KvSeq& s = P.plan.seq[i];
+    unsigned char* q_out = P.q_out + (int64_t)tok * P.q_heads * D * 2;
+    if (node >= s.ntok) {
+      for (int x = q0 * kVec + lane; x < q1 * kVec; x += 32) reinterpret_cast<uint4*>(q_out)[x] = uint4{0, 0, 0, 0};
       continue;
     }
-    const int slot = s.base + node;
-    const int page = c.table[(int64_t)s.row * c.max_pages + (slot >> c.log_page)];
-    const int64_t at = kv_offset(c, P.layer, page, 0) + (int64_t)(slot & (c.page - 1)) * D * 2;
-    const int64_t head_bytes = (int64_t)c.page * D * 2;
-    if (P.interleaved || half % 8 == 0) {
-      // a vector of 8 elements; in the half layout the one that holds the
-      // lower elements of 8 pairs takes their upper ones too
-      for (int x = tid; x < heads * vec; x += 256) {
-        const int h = x / vec, e = x % vec * 8;
-        const unsigned char* src;
-        unsigned char* dst;
-        const bool value = h >= q_heads + c.kv_heads;
-        if (h < q_heads) {
-          src = P.q + (tok * P.q_stride + h * D) * 2;
-          dst = P.q_out + (tok * P.q_heads + h) * D * 2;
-        } else if (!value) {
-          src = P.k + (tok * P.k_stride + (h - q_heads) * D) * 2;
-          dst = c.k + at + (h - q_heads) * head_bytes;
-        } else {
-          src = P.v + (tok * P.v_stride + (h - q_heads - c.kv_heads) * D) * 2;
-          dst = c.v + at + (h - q_heads - c.kv_heads) * head_bytes;
-        }
-        if (value || e >= P.rot) {
-          *reinterpret_cast<uint4*>(dst + e * 2) = *reinterpret_cast<const uint4*>(src + e * 2);
-        } else if (P.interleaved) {
-          uint4 u = *reinterpret_cast<const uint4*>(src + e * 2);
-          uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    const int z = s.base + node, page = c.table[(int64_t)s.row * c.max_pages + (z >> c.log_page)];
+    const int64_t at = kv_offset(c, P.layer, page, 0) + (int64_t)(z & (c.page - 1)) * D * 2;
+    const int64_t pos = (int64_t)s.base + (tree ? P.plan.node[tok].x : node);
+    const unsigned char* q = P.q + (int64_t)tok * P.q_stride * 2;
+    const unsigned char* k = P.k + (int64_t)tok * P.k_stride * 2;
+    const unsigned char* v = P.v + (int64_t)tok * P.v_stride * 2;
+    __syncwarp();  // the last token's values are read
+#pragma unroll 1
+    for (int j = lane; j < half; j += 32) {
+      const uint64_t a = (uint64_t)pos * turn[j];
+      float sn, cn;
+      sincospif((float)(int64_t)a * 1.0842021724855044e-19f, &sn, &cn);  // 2^-63
+      cs[warp][j] = {cn * P.mscale, sn * P.mscale};
+    }
+    __syncwarp();
+    // heads [h0, h1) from src to dst (heads dst_head bytes apart), turned or not
+    auto heads = [&](const unsigned char* src, unsigned char* dst, int dst_head, int h0, int h1, bool turned) {
+      src += ((h0 + lane / kVec) * D + e * 8) * 2;
+      dst += (int64_t)(h0 + lane / kVec) * dst_head + e * 16;
+#pragma unroll 1
+      for (int h = h0; h < h1; h += kDeep * kStep) {
+        const int left = h1 - h - lane / kVec;
+        uint4 x[kDeep];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (e + 2 * k < P.rot) {
-              const float2 a = unpack<T>(w[k]), r = cs[e / 2 + k];
-              w[k] = pack<T>(a.x * r.x - a.y * r.y, a.x * r.y + a.y * r.x);
+        for (int y = 0; y < kDeep; ++y)
+          if (y * kStep < left) x[y] = *reinterpret_cast<const uint4*>(src + y * (kStep * D * 2));
+#pragma unroll
+        for (int y = 0; y < kDeep; ++y) {
+          if (h + y * kStep >= h1) break;  // (the whole warp)
+          uint32_t* a = reinterpret_cast<uint32_t*>(&x[y]);
+          if (turned) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (kInterleaved) {
+                const float2 f = unpack<T>(a[w]), g = cs[warp][(first + w) & 63];
+                if (first + w < half) a[w] = pack<T>(f.x * g.x - f.y * g.y, f.x * g.y + f.y * g.x);
+              } else {
+                const float2 f = unpack<T>(a[w]), o = unpack<T>(__shfl_sync(kFullMask, a[w], other & 31));
+                const float2 g0 = cs[warp][(first + 2 * w) & 63], g1 = cs[warp][(first + 2 * w + 1) & 63];
+                if (role == 1) a[w] = pack<T>(f.x * g0.x - o.x * g0.y, f.y * g1.x - o.y * g1.y);
+                if (role == 2) a[w] = pack<T>(o.x * g0.y + f.x * g0.x, o.y * g1.y + f.y * g1.x);
+              }
             }
-          *reinterpret_cast<uint4*>(dst + e * 2) = u;
-        } else if (e < half) {
-          uint4 lo = *reinterpret_cast<const uint4*>(src + e * 2);
-          uint4 hi = *reinterpret_cast<const uint4*>(src + (e + half) * 2);
-          uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
-          uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = unpack<T>(a[k]), w = unpack<T>(b[k]);
-            const float2 r0 = cs[e + 2 * k], r1 = cs[e + 2 * k + 1];
-            a[k] = pack<T>(u.x * r0.x - w.x * r0.y, u.y * r1.x - w.y * r1.y);
-            b[k] = pack<T>(u.x * r0.y + w.x * r0.x, u.y * r1.y + w.y * r1.x);
           }
-          *reinterpret_cast<uint4*>(dst + e * 2) = lo;
-          *reinterpret_cast<uint4*>(dst + (e + half) * 2) = hi;
+          if (y * kStep < left) *reinterpret_cast<uint4*>(dst) = x[y];
+          dst += (int64_t)kStep * dst_head;
         }
+        src += kDeep * kStep * D * 2;
       }
+    };
+    if (vectors) {
+      heads(q, q_out, D * 2, q0, q1, half > 0);
+      heads(k, c.k + at, head_bytes, k0, k1, half > 0);
     } else {
       // halves that do not begin on a vector: single elements
-      for (int x = tid; x < heads * D; x += 256) {
-        const int h = x / D, e = x % D;
-        const T* src;
-        T* dst;
-        const bool value = h >= q_heads + c.kv_heads;
-        if (h < q_heads) {
-          src = reinterpret_cast<const T*>(P.q) + tok * P.q_stride + h * D;
-          dst = reinterpret_cast<T*>(P.q_out) + (tok * P.q_heads + h) * D;
-        } else if (!value) {
-          src = reinterpret_cast<const T*>(P.k) + tok * P.k_stride + (h - q_heads) * D;
-          dst = reinterpret_cast<T*>(c.k + at + (h - q_heads) * head_bytes);
-        } else {
-          src = reinterpret_cast<const T*>(P.v) + tok * P.v_stride + (h - q_heads - c.kv_heads) * D;
-          dst = reinterpret_cast<T*>(c.v + at + (h - q_heads - c.kv_heads) * head_bytes);
+      auto singles = [&](const unsigned char* src, unsigned char* dst, int dst_head, int h0, int h1) {
+#pragma unroll 1
+        for (int x = h0 * D + lane; x < h1 * D; x += 32) {
+          const int h = x / D, d = x % D;
+          const T* from = reinterpret_cast<const T*>(src) + h * D;
+          T* to = reinterpret_cast<T*>(dst + (int64_t)h * dst_head);
+          if (d >= P.rot) {
+            to[d] = from[d];
+          } else if (d < half) {
+            const float a = (float)from[d], b = (float)from[d + half];
+            const float2 g = cs[warp][d];
+            to[d] = (T)(a * g.x - b * g.y);
+            to[d + half] = (T)(a * g.y + b * g.x);
+          }
         }
-        if (value || e >= P.rot) {
-          dst[e] = src[e];
-        } else if (e < half) {
-          const float a = (float)src[e], b = (float)src[e + half];
-          const float2 r = cs[e];
-          dst[e] = (T)(a * r.x - b * r.y);
-          dst[e + half] = (T)(a * r.y + b * r.x);
-        }
-      }
+      };
+      singles(q, q_out, D * 2, q0, q1);
+      singles(k, c.k + at, head_bytes, k0, k1);
     }
+    heads(v, c.v + at, head_bytes, k0, k1, false);
   }
+}
+
+template <typename T>
+void (*append_for(int D, bool interleaved))(AppendParams) {
+  if (D == 64) return interleaved ? append_kernel<T, 64, true> : append_kernel<T, 64, false>;
+  return interleaved ? append_kernel<T, 128, true> : append_kernel<T, 128, false>;
 }
 
 inline bool bad_rows(const KvView& c, const int32_t* d_rows, int32_t n) {
@@ -604,10 +644,12 @@ int kv_reserve(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t 
   ReserveWs w;
   if (ws_bytes < reserve_layout(c, n, d_workspace, &w)) return SAMSPEC_ESIZE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  reserve_kernel<<<1, 1024, 0, s>>>(c, d_rows, n, N, d_n_tok, d_status, w);
   const int64_t items = (int64_t)n * c.layers * 2 * c.kv_heads;
   const int64_t ctas = (items + 7) / 8;
-  copy_pages_kernel<<<(unsigned)(ctas < kKvCtas * 8 ? ctas : kKvCtas * 8), 256, 0, s>>>(c, w.cow);
+  if (launch_after(reserve_kernel, 1, 1024, 0, s, c, d_rows, n, N, d_n_tok, d_status, w) != cudaSuccess ||
+      launch_after(copy_pages_kernel, (unsigned)(ctas < kKvCtas * 8 ? ctas : kKvCtas * 8), 256, 0, s, c, w.cow) !=
+          cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 
@@ -618,7 +660,9 @@ int kv_fork(const kv_cache* cache, const int32_t* d_src, const int32_t* d_dst, i
   if (rc != SAMSPEC_OK) return rc;
   if (!d_src || !d_dst) return SAMSPEC_EINVAL;
   if (n < 1 || n > (1 << 20)) return SAMSPEC_ESIZE;
-  fork_kernel<<<n, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(c, d_src, d_dst, n, d_status);
+  if (launch_after(fork_kernel, n, 256, 0, reinterpret_cast<cudaStream_t>(stream), c, d_src, d_dst, n, d_status) !=
+      cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 
@@ -632,14 +676,15 @@ int kv_commit(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N
   if (bad_rows(c, d_rows, n) || N < 1 || N > (d_path ? 32 : 1 << 30)) return SAMSPEC_ESIZE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d_path) {
-    const int64_t ctas = ((int64_t)n * c.layers * 2 * c.kv_heads + 7) / 8;
+    const int64_t ctas = (int64_t)n * (((int64_t)c.layers * 2 * c.kv_heads + kMoveItems - 1) / kMoveItems);
     if (ctas >= ((int64_t)1 << 31)) return SAMSPEC_ESIZE;
-    if (c.head_dim == 64)
-      move_path_kernel<64><<<(unsigned)ctas, 256, 0, s>>>(c, d_rows, n, N, d_accept_len, d_path, d_status);
-    else
-      move_path_kernel<128><<<(unsigned)ctas, 256, 0, s>>>(c, d_rows, n, N, d_accept_len, d_path, d_status);
+    if (launch_after(c.head_dim == 64 ? move_path_kernel<64> : move_path_kernel<128>, (unsigned)ctas, 256, 0, s, c,
+                     d_rows, n, N, d_accept_len, d_path, d_status) != cudaSuccess)
+      return SAMSPEC_ECUDA;
   }
-  set_len_kernel<<<(n + 7) / 8, 256, 0, s>>>(c, d_rows, n, N, d_accept_len, d_path, nullptr, d_status);
+  if (launch_after(set_len_kernel, (n + 7) / 8, 256, 0, s, c, d_rows, n, N, d_accept_len, d_path, nullptr, d_status) !=
+      cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 
@@ -649,8 +694,9 @@ int kv_truncate(const kv_cache* cache, const int32_t* d_rows, int32_t n, const i
   const int rc = kv_view(cache, &c);
   if (rc != SAMSPEC_OK) return rc;
   if (bad_rows(c, d_rows, n)) return SAMSPEC_ESIZE;
-  set_len_kernel<<<(n + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      c, d_rows, n, 0, nullptr, nullptr, d_new_len, d_status);
+  if (launch_after(set_len_kernel, (n + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream), c, d_rows, n, 0,
+                   nullptr, nullptr, d_new_len, d_status) != cudaSuccess)
+    return SAMSPEC_ECUDA;
   return launched();
 }
 
@@ -681,7 +727,6 @@ int kv_append(const kv_cache* cache, int32_t layer, const void* d_plan, int32_t 
   P.N = N;
   P.q_heads = q_heads;
   P.rot = rot;
-  P.interleaved = layout == SAMSPEC_ROPE_INTERLEAVED;
   P.q = static_cast<const unsigned char*>(d_q);
   P.q_out = static_cast<unsigned char*>(d_q_out);
   P.k = static_cast<const unsigned char*>(d_k);
@@ -691,13 +736,17 @@ int kv_append(const kv_cache* cache, int32_t layer, const void* d_plan, int32_t 
   P.v_stride = v_stride;
   P.inv_freq = d_inv_freq;
   P.mscale = mscale;
+  // few tokens: a warp takes a part of a token's heads, as long as all warps run
+  // at once (16 an SM; a second wave of 2048 tokens in quarters took 14.5 us, one
+  // wave of whole ones 8)
   const int64_t toks = (int64_t)n * N;
-  const unsigned grid = (unsigned)(toks < kKvCtas * 8 ? toks : kKvCtas * 8);
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cache->dtype == SAMSPEC_BF16)
-    append_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(P);
-  else
-    append_kernel<__half><<<grid, 256, 0, s>>>(P);
+  P.parts = toks * 4 <= kKvCtas * 16 ? 4 : toks * 2 <= kKvCtas * 16 ? 2 : 1;
+  const int64_t ctas = (toks * P.parts + 7) / 8;
+  const unsigned grid = (unsigned)(ctas < kKvCtas * 8 ? ctas : kKvCtas * 8);
+  const bool inter = layout == SAMSPEC_ROPE_INTERLEAVED;
+  void (*kernel)(AppendParams) = cache->dtype == SAMSPEC_BF16 ? append_for<__nv_bfloat16>(P.c.head_dim, inter)
+                                                              : append_for<__half>(P.c.head_dim, inter);
+  if (launch_after(kernel, grid, 256, 0, reinterpret_cast<cudaStream_t>(stream), P) != cudaSuccess) return SAMSPEC_ECUDA;
   return launched();
 }
 

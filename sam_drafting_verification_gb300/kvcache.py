@@ -23,7 +23,7 @@ import sys
 import torch
 
 from . import _binding as _b
-from . import _cuda_device, _ptr, _req
+from . import _cuda_device, _req
 
 _pkg = sys.modules[__package__]
 _DTYPES = {torch.bfloat16: _b.BF16, torch.float16: _b.F16}
@@ -91,7 +91,7 @@ class KVPlan:
     def __init__(self, n, N, q_heads, grouped, buf):
         self.n, self.N, self.q_heads, self.grouped, self.buf = n, N, q_heads, grouped, buf
         self.bytes = buf.numel()
-        self.ptr = ctypes.c_void_p(buf.data_ptr())
+        self.ptr = buf.data_ptr()
 
     @property
     def status(self):
@@ -155,33 +155,49 @@ class KVCache:
                                     _DTYPES[k.dtype], *(int(x) for x in (layers, pages, page, kv_heads, head_dim,
                                                                          seqs, max_pages)))
         self._ref = ctypes.byref(self._desc)
+        self._bytes = {}   # workspace sizes by call sizes
 
     # -- helpers ---------------------------------------------------------------
     def _call(self, name, *args):
         """The entry point on the device's current stream, with that device
         current for the launch."""
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
-                rc = getattr(self.lib, name)(self._ref, *args, _pkg._stream(self.device))
-        else:
+        index = self.device.index
+        if self.device.type != "cuda":
             rc = getattr(self.lib, name)(self._ref, *args, _pkg._stream(self.device))
-        _b.check(rc, name)
+        elif index == torch.cuda.current_device():
+            rc = getattr(self.lib, name)(self._ref, *args, _pkg._raw_stream(index))
+        else:
+            with torch.cuda.device(self.device):
+                rc = getattr(self.lib, name)(self._ref, *args, _pkg._raw_stream(index))
+        if rc != _b.OK:
+            _b.check(rc, name)
 
     def _i32(self, t, name, shape):
-        return _req(t, torch.int32, name, shape, self.device)
+        # the common case in a few comparisons; _req says what is wrong
+        try:
+            if t.dtype is torch.int32 and t.shape == shape and t.device == self.device and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        return _req(t, torch.int32, name, shape, self.device).data_ptr()
 
     def _rows(self, rows, n=None):
+        """(how many sequences a call names, the pointer)"""
         if rows is None:
-            return self.seqs if n is None else n
-        _req(rows, torch.int32, "rows", None if n is None else (n,), self.device)
-        if rows.dim() != 1:
-            raise ValueError("rows must be [n]")
-        return int(rows.shape[0])
+            n = self.seqs if n is None else n
+            if n > self.seqs:
+                raise ValueError(f"{n} sequences named, the cache has {self.seqs}")
+            return n, None
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise ValueError("rows must be an int32 tensor [n]")
+        n = rows.shape[0] if n is None else n
+        return n, self._i32(rows, "rows", (n,))
 
     def _status(self, n, out):
         if out is None:
             return torch.empty(n, dtype=torch.int32, device=self.device)
-        return self._i32(out, "out", (n,))
+        self._i32(out, "out", (n,))
+        return out
 
     # -- pages -----------------------------------------------------------------
     def reserve(self, rows, n_tok, out=None):
@@ -189,24 +205,30 @@ class KVCache:
         committed ones of sequences `rows` (int32 [n], or None for all).  Returns
         the status words int32 [n]: ST_CAPACITY where pages ran out."""
         if isinstance(n_tok, torch.Tensor):
-            n = self._rows(rows, int(n_tok.shape[0]) if rows is None and n_tok.dim() == 1 else None)
-            self._i32(n_tok, "n_tok", (n,))
-            most = min(self.max_pages * self.page, 1 << 30)
+            if n_tok.dim() != 1:
+                raise ValueError("n_tok must be [n]")
+            n, rp = self._rows(rows, n_tok.shape[0])
+            most, np = min(self.max_pages * self.page, 1 << 30), self._i32(n_tok, "n_tok", (n,))
         else:
-            n, most, n_tok = self._rows(rows), int(n_tok), None
+            n, rp = self._rows(rows)
+            most, np = int(n_tok), None
         st = self._status(n, out)
-        ws = torch.empty(max(1, int(self.lib.kv_reserve_workspace_bytes(self._ref, n))), dtype=torch.uint8,
-                         device=self.device)
-        self._call("kv_reserve", _ptr(rows), n, most, _ptr(n_tok), _ptr(st), _ptr(ws), ws.numel())
+        need = self._bytes.get(n)
+        if need is None:
+            need = self._bytes[n] = int(self.lib.kv_reserve_workspace_bytes(self._ref, n))
+        ws = torch.empty(max(1, need), dtype=torch.uint8, device=self.device)
+        self._call("kv_reserve", rp, n, most, np, st.data_ptr(), ws.data_ptr(), need)
         return st
 
     def fork(self, src, dst, out=None):
         """Sequences dst (int32 [n], empty) become copies of src (int32 [n]),
         sharing their pages.  Returns the status words int32 [n]."""
-        n = self._rows(src)
-        self._rows(dst, n)
+        if src is None or dst is None:
+            raise ValueError("src and dst must be int32 tensors [n]")
+        n, sp = self._rows(src)
+        _, dp = self._rows(dst, n)
         st = self._status(n, out)
-        self._call("kv_fork", _ptr(src), _ptr(dst), n, _ptr(st))
+        self._call("kv_fork", sp, dp, n, st.data_ptr())
         return st
 
     def commit(self, rows, accept_len, path=None, out=None):
@@ -214,26 +236,32 @@ class KVCache:
         accept_len int32 [n] (spec_verify, spec_verify_tree; -1 keeps nothing),
         path int32 [n, N] (spec_verify_tree; None for chains).  Returns the
         status words int32 [n]."""
-        n = self._rows(rows, int(accept_len.shape[0]) if accept_len.dim() == 1 else None)
-        self._i32(accept_len, "accept_len", (n,))
-        N = 1 << 30
+        if not isinstance(accept_len, torch.Tensor) or accept_len.dim() != 1:
+            raise ValueError("accept_len must be an int32 tensor [n]")
+        n, rp = self._rows(rows, accept_len.shape[0])
+        ap, pp, N = self._i32(accept_len, "accept_len", (n,)), None, 1 << 30
         if path is not None:
-            _req(path, torch.int32, "path", None, self.device)
-            if path.dim() != 2 or path.shape[0] != n:
-                raise ValueError("path must be [n, N]")
-            N = int(path.shape[1])
+            if not isinstance(path, torch.Tensor) or path.dim() != 2:
+                raise ValueError("path must be an int32 tensor [n, N]")
+            N = path.shape[1]
+            pp = self._i32(path, "path", (n, N))
         st = self._status(n, out)
-        self._call("kv_commit", _ptr(rows), n, N, _ptr(accept_len), _ptr(path), _ptr(st))
+        self._call("kv_commit", rp, n, N, ap, pp, st.data_ptr())
         return st
 
     def truncate(self, rows, new_len=None, out=None):
         """Cuts sequences to at most new_len tokens (int32 [n]; None: empties
         them) and gives back the pages behind, reserved ones too."""
-        n = self._rows(rows, None if new_len is None else int(new_len.shape[0]))
+        lp = None
         if new_len is not None:
-            self._i32(new_len, "new_len", (n,))
+            if not isinstance(new_len, torch.Tensor) or new_len.dim() != 1:
+                raise ValueError("new_len must be an int32 tensor [n]")
+            n, rp = self._rows(rows, new_len.shape[0])
+            lp = self._i32(new_len, "new_len", (n,))
+        else:
+            n, rp = self._rows(rows)
         st = self._status(n, out)
-        self._call("kv_truncate", _ptr(rows), n, _ptr(new_len), _ptr(st))
+        self._call("kv_truncate", rp, n, lp, st.data_ptr())
         return st
 
     # -- a pass ------------------------------------------------------------------
@@ -244,74 +272,76 @@ class KVCache:
         group int32 [n]: consecutive sequences of one number read the pages
         that they share once.  out: the plan of an earlier call with the same
         sizes, written again in place."""
-        n = self._rows(rows)
         N, q_heads = int(N), int(q_heads)
-        if n_tok is not None:
-            self._i32(n_tok, "n_tok", (n,))
-        fc = ns = None
-        if tree is not None:
-            if n_tok is not None:
-                n_tok = None   # every node of a tree takes part
-            fc, ns = tree
-            self._i32(fc, "first_child", (n, N))
-            self._i32(ns, "next_sibling", (n, N))
+        n, rp = self._rows(rows)
+        np = fp = sp = gp = None
+        if tree is not None:    # every node takes part
+            fp = self._i32(tree[0], "first_child", (n, N))
+            sp = self._i32(tree[1], "next_sibling", (n, N))
+        elif n_tok is not None:
+            np = self._i32(n_tok, "n_tok", (n,))
         if group is not None:
-            self._i32(group, "group", (n,))
+            gp = self._i32(group, "group", (n,))
         if out is None:
-            need = int(self.lib.kv_plan_bytes(self._ref, n, N, q_heads, group is not None))
+            key = (n, N, q_heads, gp is not None)
+            need = self._bytes.get(key)
+            if need is None:
+                need = self._bytes[key] = int(self.lib.kv_plan_bytes(self._ref, n, N, q_heads, gp is not None))
             if need == 0:
                 raise _b.SamspecError(f"sizes outside the limits: n={n}, N={N}, q_heads={q_heads}")
-            out = KVPlan(n, N, q_heads, group is not None,
-                         torch.empty(need, dtype=torch.uint8, device=self.device))
+            out = KVPlan(n, N, q_heads, gp is not None, torch.empty(need, dtype=torch.uint8, device=self.device))
         elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.buf.device != self.device or \
-                (group is not None and not out.grouped):
+                (gp is not None and not out.grouped):
             raise ValueError("out: a plan of other sizes")
-        self._call("kv_plan", _ptr(rows), n, N, q_heads, _ptr(n_tok), _ptr(fc), _ptr(ns), _ptr(group), out.ptr,
-                   out.bytes)
+        self._call("kv_plan", rp, n, N, q_heads, np, fp, sp, gp, out.ptr, out.bytes)
         return out
 
     def _tokens(self, t, name, plan, heads):
         """t [n, N, heads, head_dim] of the cache's dtype, checked; its token
         stride in elements.  A view into a wider projection output will do."""
-        if not isinstance(t, torch.Tensor) or not _pkg._is_cuda(t):
+        shape = (plan.n, plan.N, heads, self.head_dim)
+        if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype != self.dtype:
+        if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
-        if tuple(t.shape) != (plan.n, plan.N, heads, self.head_dim):
-            raise ValueError(f"{name} must have shape {(plan.n, plan.N, heads, self.head_dim)}, got {tuple(t.shape)}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        s = t.stride()
-        step = s[1] if plan.N > 1 else s[0] if plan.n > 1 else heads * self.head_dim
-        if s[3] != 1 or (heads > 1 and s[2] != self.head_dim) or (plan.n > 1 and s[0] != plan.N * step) \
-                or step < heads * self.head_dim:
+        s, row = t.stride(), heads * self.head_dim
+        step = s[1] if plan.N > 1 else s[0] if plan.n > 1 else row
+        if s[3] != 1 or (heads > 1 and s[2] != self.head_dim) or (plan.n > 1 and s[0] != plan.N * step) or step < row:
             raise ValueError(f"{name}: tokens must follow one another at one stride, heads and elements without gaps")
         return step
+
+    def _output(self, out, plan):
+        shape = (plan.n, plan.N, plan.q_heads, self.head_dim)
+        if out is None:
+            return torch.empty(shape, dtype=self.dtype, device=self.device)
+        return _req(out, self.dtype, "out", shape, self.device)
 
     def append(self, layer: int, plan: KVPlan, q, k, v, rope: Rope | None = None, out=None):
         """Writes the new tokens' keys and values k, v [n, N, kv_heads, head_dim]
         into their slots of `layer`, keys turned to their positions, and returns
         the turned queries (q [n, N, q_heads, head_dim]; out may be q itself
         where that is contiguous; None: keys and values only)."""
-        qs = 0
+        qs, qp, op = 0, None, None
         if q is not None:
             qs = self._tokens(q, "q", plan, plan.q_heads)
-            if out is None:
-                out = torch.empty((plan.n, plan.N, plan.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
-            else:
-                _req(out, self.dtype, "out", q.shape, self.device)
+            out = self._output(out, plan)
+            qp, op = q.data_ptr(), out.data_ptr()
         else:
             out = None
         ks, vs = self._tokens(k, "k", plan, self.kv_heads), self._tokens(v, "v", plan, self.kv_heads)
         rot, layout, mscale, freq = 0, 0, 1.0, None
         if rope is not None:
-            rot, layout, mscale, freq = rope.rot, rope.layout, rope.mscale, rope.inv_freq
-            if rot > self.head_dim:
+            if rope.rot > self.head_dim:
                 raise ValueError("rope: more pairs than the head has")
-            if freq.device != self.device:
-                raise ValueError(f"rope must be on {self.device}, got {freq.device}")
-        self._call("kv_append", int(layer), plan.ptr, plan.n, plan.N, plan.q_heads, _ptr(q), qs, _ptr(out), _ptr(k),
-                   ks, _ptr(v), vs, _ptr(freq), rot, layout, mscale)
+            if rope.inv_freq.device != self.device:
+                raise ValueError(f"rope must be on {self.device}, got {rope.inv_freq.device}")
+            rot, layout, mscale, freq = rope.rot, rope.layout, rope.mscale, rope.inv_freq.data_ptr()
+        self._call("kv_append", int(layer), plan.ptr, plan.n, plan.N, plan.q_heads, qp, qs, op, k.data_ptr(), ks,
+                   v.data_ptr(), vs, freq, rot, layout, mscale)
         return out
 
     def attend(self, layer: int, plan: KVPlan, q, scale: float | None = None, out=None):
@@ -319,10 +349,7 @@ class KVCache:
         1 / sqrt(head_dim) unless given).  Returns [n, N, q_heads, head_dim];
         tokens that take no part get zeros."""
         qs = self._tokens(q, "q", plan, plan.q_heads)
-        if out is None:
-            out = torch.empty((plan.n, plan.N, plan.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
-        else:
-            _req(out, self.dtype, "out", q.shape, self.device)
-        self._call("kv_attend", int(layer), plan.ptr, plan.bytes, plan.n, plan.N, plan.q_heads, _ptr(q), qs,
-                   self.head_dim ** -0.5 if scale is None else float(scale), _ptr(out))
+        out = self._output(out, plan)
+        self._call("kv_attend", int(layer), plan.ptr, plan.bytes, plan.n, plan.N, plan.q_heads, q.data_ptr(), qs,
+                   self.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr())
         return out
