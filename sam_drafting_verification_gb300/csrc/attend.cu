@@ -1041,8 +1041,8 @@ __global__ void __launch_bounds__(384, 1)
       if (!direct) {
         // a whole unit that is joined with others: the store of its kind; else
         // the first segment of a CTA's share, or its last
-        slot = nb == sg.t.blocks ? 2 * kKvCtas * kTileRows + (kind == 1 ? P.plan.store : 0) + q_row
-                                 : (int64_t)(2 * blockIdx.x + (seg > 0)) * kTileRows + (rows2 ? kRows * x0 : 0) + row;
+        slot = nb == sg.t.blocks ? (int64_t)2 * kKvCtas * P.plan.slot_rows + (kind == 1 ? P.plan.store : 0) + q_row
+                                 : (int64_t)(2 * blockIdx.x + (seg > 0)) * P.plan.slot_rows + (rows2 ? kRows * x0 : 0) + row;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int cols = rows2 ? D : D / 2, d0 = rows2 ? 0 : w * (D / 2);
@@ -1112,26 +1112,111 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 9) tmem_free(tmem, 512);
 }
 
-// Rows of units that were cut among CTAs, or that have a shared part: their
-// partial results joined.  Rows that were written where they were computed are
-// passed over, those of no token become zeros.  A warp takes 8 rows: a lane
-// finds where one row's parts lie, then the warp adds up one row after the
-// other, the loads of up to 4 parts in flight at once.  (Calls of few rows
-// give a warp fewer.)
-#ifndef KJR
-#define KJR 8
-#endif
-constexpr int kJoinRows = KJR;
+// ---- joining partial results ---------------------------------------------------
+// The CTAs [c0, c1] that hold the blocks of unit (tile t, head h): those of its
+// first and its last block, each the last that begins at or before it.
+__device__ __forceinline__ int2 unit_ctas(const KvTile& t, int h, int ctas, int cost) {
+  const int bc = block_cost(t);
+  const int64_t b0 = t.cost0 + h * (t.blocks * bc + kUnitCost) + kUnitCost + 1;
+  return {(int)((b0 * ctas - 1) / cost), (int)(((b0 + (t.blocks - 1) * bc) * ctas - 1) / cost)};
+}
+// Row `at` of a cut unit: where its part of CTA c0 lies (that one's first
+// segment, or its last), and of CTA c0 + 1 (the first; the others follow 2 *
+// slot_rows apart).
+__device__ __forceinline__ int2 part_slots(const PlanView& p, int ti, int h, int c0, int at) {
+  const int4 st = p.start[c0];
+  const bool begins = st.x == ti && st.y == h && st.z == 0;
+  return {(2 * c0 + !begins) * p.slot_rows + at, 2 * (c0 + 1) * p.slot_rows + at};
+}
+
+// A row's parts added up by a warp, four in flight at once: `cnt` of them, the
+// first n0 from f0, then s0 on, the others from f1, then s1 on.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows) {
+__device__ __forceinline__ void join_row(const AttendParams& P, int64_t row, int cnt, int n0, int f0, int s0, int f1,
+                                         int s1, int lane) {
   using H = Type16<T>;
   constexpr int kPer = D / 32;
   struct alignas(4 * kPer) Vec {
     float x[kPer];
   };
+  float m = -INFINITY, l = 0.f, o[kPer] = {};
+  for (int q = 0; q < cnt; q += 4) {
+    float2 z[4];
+    Vec a[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = q + e;
+      z[e] = {-INFINITY, 0.f};
+      if (k < cnt) {
+        const int j = k < n0 ? k : k - n0;
+        const int64_t slot = j == 0 ? (k < n0 ? f0 : f1) : (k < n0 ? s0 : s1) + (int64_t)(j - 1) * 2 * P.plan.slot_rows;
+        z[e] = P.plan.ml[slot];
+        a[e] = *reinterpret_cast<const Vec*>(P.plan.o + slot * D + lane * kPer);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (q + e < cnt) {
+        const float mn = fmaxf(m, z[e].x), mm = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - mm), g = exp2f(z[e].x - mm);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) o[d] = o[d] * f + a[e].x[d] * g;
+        l = l * f + z[e].y * g;
+        m = mn;
+      }
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(P.out + row * D * 2) + lane * (kPer / 2);
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+}
+
+// Without groups only units that were cut among CTAs are joined: where a share
+// begins inside a unit, and no share before it does in the same one, the CTA
+// (boundary, 1 of kJoinParts) joins a part of that unit's rows.  The CTAs behind
+// these write the zeros of tokens that take no part.
+constexpr int kJoinParts = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_cut_kernel(AttendParams P) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_previous();
+  let_next_start();
+  if (blockIdx.x >= (kKvCtas - 1) * kJoinParts) {
+    // 4 tokens a warp (32 took 43 us where half of 4000 tokens take no part)
+    const int t0 = ((blockIdx.x - (kKvCtas - 1) * kJoinParts) * 8 + warp) * 4, tok = t0 + lane;
+    bool dead = false;
+    if (lane < 4 && tok < P.n * P.N) dead = tok % P.N >= P.plan.seq[tok / P.N].ntok;
+    for (uint32_t todo = __ballot_sync(kFullMask, dead); todo; todo &= todo - 1) {
+      uint4* out = reinterpret_cast<uint4*>(P.out + (int64_t)(t0 + __ffs(todo) - 1) * P.q_heads * D * 2);
+      for (int x = lane; x < P.q_heads * (D / 8); x += 32) out[x] = uint4{0, 0, 0, 0};
+    }
+    return;
+  }
+  const int b = blockIdx.x / kJoinParts + 1, part = blockIdx.x % kJoinParts;
+  const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
+  if (b >= ctas) return;
+  const int4 st = P.plan.start[b], before = P.plan.start[b - 1];
+  if (st.z == 0 || (before.x == st.x && before.y == st.y && before.z > 0)) return;
+  const KvTile t = P.plan.tile[st.x];
+  const int2 c = unit_ctas(t, st.y, ctas, cost);
+  const int tt = tile_tokens(P.rep), rows = t.toks * P.rep;
+  for (int x = part * 8 + warp; x < rows; x += 8 * kJoinParts) {
+    const int lt = x / P.rep, j = x % P.rep;
+    const int2 s = part_slots(P.plan, st.x, st.y, c.x, lt / tt * kRows + lt % tt * P.rep + j);
+    const int64_t row = ((int64_t)t.tok0 + lt) * P.q_heads + st.y * P.rep + j;
+    join_row<T, D>(P, row, c.y - c.x + 1, 0, 0, 0, s.x, s.y, lane);
+  }
+}
+
+// With groups: a warp takes 8 rows, a lane finds where one row's parts lie
+// (none where it was written at once), then the warp adds up one after the
+// other.
+constexpr int kJoinRows = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_rows_kernel(AttendParams P) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * warp_rows;
+  const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoinRows;
   wait_for_previous();
   let_next_start();
   if (r0 >= rows) return;
@@ -1139,7 +1224,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
   // the own keys where the first part lies and where the others begin
   int parts = -1, first[2] = {0, 0}, rest[2] = {0, 0}, cnt[2] = {0, 0};
   const int64_t mine = r0 + lane;
-  if (lane < warp_rows && mine < rows) {
+  if (lane < kJoinRows && mine < rows) {
     const int hq = (int)(mine % P.q_heads);
     const int64_t tok = mine / P.q_heads;
     const int i = (int)(tok / P.N), node = (int)(tok % P.N);
@@ -1155,23 +1240,15 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
         const int ft = p ? node : (i - s.leader) * P.N + node, lt = ft % (2 * tt);
         const int at = lt / tt * kRows + lt % tt * P.rep + hq % P.rep;  // its row of the unit
         const int ti = (p ? P.plan.suf0[i] : P.plan.pre0[s.leader]) + ft / (2 * tt);
-        const KvTile t = P.plan.tile[ti];
-        const int bc = block_cost(t);
-        const int b0 = t.cost0 + h * (t.blocks * bc + kUnitCost);  // the unit's costs begin
-        // the CTAs that hold its first and its last block: the last that
-        // begins at or before each
-        const int c0 = (int)((((int64_t)b0 + kUnitCost + 1) * ctas - 1) / cost);
-        const int c1 = (int)((((int64_t)b0 + kUnitCost + (t.blocks - 1) * bc + 1) * ctas - 1) / cost);
-        cnt[p] = c1 - c0 + 1;
-        if (c0 == c1) {
+        const int2 c = unit_ctas(P.plan.tile[ti], h, ctas, cost);
+        cnt[p] = c.y - c.x + 1;
+        if (c.x == c.y) {
           if (s.shared == 0) cnt[p] = 0;
-          first[p] = (int)(2 * kKvCtas * kTileRows + (p ? 0 : P.plan.store) + mine);
+          first[p] = (int)(2 * kKvCtas * P.plan.slot_rows + (p ? 0 : P.plan.store) + mine);
         } else {
-          // the first segment of a CTA's share, or its last
-          const int4 st = P.plan.start[c0];
-          const bool begins = st.x == ti && st.y == h && st.z == 0;
-          first[p] = (2 * c0 + !begins) * kTileRows + at;
-          rest[p] = 2 * (c0 + 1) * kTileRows + at;
+          const int2 f = part_slots(P.plan, ti, h, c.x, at);
+          first[p] = f.x;
+          rest[p] = f.y;
         }
       }
       parts = cnt[0] + cnt[1];
@@ -1183,36 +1260,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttendParams P, int warp_rows
     const int n = __shfl_sync(kFullMask, parts, w), n0 = __shfl_sync(kFullMask, cnt[0], w);
     const int f0 = __shfl_sync(kFullMask, first[0], w), f1 = __shfl_sync(kFullMask, first[1], w);
     const int s0 = __shfl_sync(kFullMask, rest[0], w), s1 = __shfl_sync(kFullMask, rest[1], w);
-    float m = -INFINITY, l = 0.f, o[kPer] = {};
-    for (int q = 0; q < n; q += 4) {
-      float2 z[4];
-      Vec a[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = q + e;
-        z[e] = {-INFINITY, 0.f};
-        if (k < n) {
-          const int j = k < n0 ? k : k - n0;
-          const int64_t slot = j == 0 ? (k < n0 ? f0 : f1) : (k < n0 ? s0 : s1) + (j - 1) * 2 * kTileRows;
-          z[e] = P.plan.ml[slot];
-          a[e] = *reinterpret_cast<const Vec*>(P.plan.o + slot * D + lane * kPer);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (q + e < n) {
-          const float mn = fmaxf(m, z[e].x), mm = mn == -INFINITY ? 0.f : mn;
-          const float f = exp2f(m - mm), g = exp2f(z[e].x - mm);
-#pragma unroll
-          for (int d = 0; d < kPer; ++d) o[d] = o[d] * f + a[e].x[d] * g;
-          l = l * f + z[e].y * g;
-          m = mn;
-        }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(P.out + (r0 + w) * D * 2) + lane * (kPer / 2);
-#pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+    join_row<T, D>(P, r0 + w, n, n0, f0, s0, f1, s1, lane);
   }
 }
 
@@ -1271,12 +1319,15 @@ int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, const C
       cudaSuccess)
     return SAMSPEC_ECUDA;
   P.lazy = Type16<T>::kLazy / P.scale_log2;
-  const int64_t rows = (int64_t)P.n * P.N * P.q_heads;
-  const int per = rows >= kKvCtas * 32 * 8 ? kJoinRows : rows >= kKvCtas * 32 * 2 ? 2 : 1;
-  if (launch_after(attend_kernel<T, D>, kKvCtas, 384, Ring<D>::kBytes, s, P, mk, mv, mq) != cudaSuccess ||
-      launch_after(join_kernel<T, D>, (unsigned)((rows + 8 * per - 1) / (8 * per)), 256, 0, s, P, per) != cudaSuccess)
+  if (launch_after(attend_kernel<T, D>, kKvCtas, 384, Ring<D>::kBytes, s, P, mk, mv, mq) != cudaSuccess)
     return SAMSPEC_ECUDA;
-  return launched();
+  const int64_t toks = (int64_t)P.n * P.N;
+  const cudaError_t e =
+      P.plan.store ? launch_after(join_rows_kernel<T, D>, (unsigned)((toks * P.q_heads + 8 * kJoinRows - 1) / (8 * kJoinRows)),
+                                  256, 0, s, P)
+                   : launch_after(join_cut_kernel<T, D>, (unsigned)((kKvCtas - 1) * kJoinParts + (toks + 31) / 32), 256, 0,
+                                  s, P);
+  return e == cudaSuccess ? launched() : SAMSPEC_ECUDA;
 }
 
 // the layout that plan_bytes bytes were asked for

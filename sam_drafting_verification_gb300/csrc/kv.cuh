@@ -138,6 +138,7 @@ enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4,
 struct PlanLayout {
   size_t status, hdr, seq, node, suf0, pre0, tile, start, ml, o, bytes;
   int32_t max_tiles;
+  int32_t slot_rows;  // rows of a cut unit's part
   int64_t store;      // rows of each of the two stores of whole units (grouped plans)
   int64_t part_rows;  // rows of partial results: two per CTA, then the stores
 };
@@ -159,7 +160,9 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
   if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
   p.max_tiles = (int32_t)(suf + pre);
   p.store = grouped ? (int64_t)n * N * q_heads : 0;
-  p.part_rows = 2 * kKvCtas * kTileRows + 2 * p.store;
+  // a unit's rows: its first tile's from 0 on, its second's from kRows
+  p.slot_rows = grouped || N > unit / 2 ? kTileRows : (int32_t)(N * rep);
+  p.part_rows = (int64_t)2 * kKvCtas * p.slot_rows + 2 * p.store;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at = kv_align(at + bytes); return o; };
   p.status = take(4 * (size_t)n);
@@ -187,7 +190,7 @@ struct PlanView {
   int4* start;     // where each CTA's share begins: tile, head, block
   float2* ml;      // partial results: running maximum (base 2) and sum ...
   float* o;        // ... and the sums of p v
-  int32_t max_tiles;
+  int32_t slot_rows;
   int64_t store;
 };
 inline PlanView plan_view(void* d_plan, const PlanLayout& p) {
@@ -197,7 +200,7 @@ inline PlanView plan_view(void* d_plan, const PlanLayout& p) {
           reinterpret_cast<int32_t*>(b + p.suf0),   reinterpret_cast<int32_t*>(b + p.pre0),
           reinterpret_cast<KvTile*>(b + p.tile),    reinterpret_cast<int4*>(b + p.start),
           reinterpret_cast<float2*>(b + p.ml),      reinterpret_cast<float*>(b + p.o),
-          p.max_tiles,                              p.store};
+          p.slot_rows,                              p.store};
 }
 
 }  // namespace samspec

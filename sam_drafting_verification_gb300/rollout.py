@@ -17,6 +17,16 @@ with rows (int32 [n], the automata / sequences of this step), n_done (int64
 [n], tokens each has generated so far), draft (int32 [n, K]) and draft_len
 (int32 [n]); row j of a sequence's logits scores the token after its first j
 drafts.
+
+With a KVCache the loop also keeps the cache: it reserves each step's slots,
+plans the pass, commits what was accepted and frees finished sequences.  The
+model then gets what such a pass works on:
+
+    model(rows, n_done, tokens, n_tok, plan) -> logits [n, K+1, V]
+
+with tokens (int32 [n, K+1]: the last token, which the cache does not hold yet,
+and the drafts, -1 behind them), n_tok (int32 [n], 1 + draft_len) and the plan
+for cache.append and cache.attend.
 """
 from __future__ import annotations
 
@@ -24,7 +34,7 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import SamBatch, verify_workspace
+from . import KVCache, SamBatch, verify_workspace
 
 
 def speculation_k(n_active: int, threshold: int | None, K: int) -> int:
@@ -46,9 +56,20 @@ class RolloutResult:
 
 class Rollout:
     def __init__(self, batch: SamBatch, model, K: int = 3, threshold: int | None = None,
-                 temperature: float = 0.0, seed: int = 0, eos: int | None = None):
+                 temperature: float = 0.0, seed: int = 0, eos: int | None = None,
+                 cache: KVCache | None = None, q_heads: int | None = None, last=None, group=None):
+        """cache: row b holds sequence b's prompt but for its last token, which
+        is last[b] (int32 [B], on the device).  q_heads: the model's query
+        heads.  group (int32 [B], optional): sequences of one number that
+        follow one another share pages (KVCache.plan)."""
         self.batch, self.model, self.K = batch, model, int(K)
         self.threshold, self.temperature, self.seed, self.eos = threshold, float(temperature), int(seed), eos
+        self.cache, self.q_heads, self.last, self.group = cache, q_heads, last, group
+        if cache is not None:
+            if q_heads is None or last is None:
+                raise ValueError("a cache needs q_heads and last")
+            if cache.seqs < batch.B:
+                raise ValueError(f"the cache has {cache.seqs} sequences, the batch {batch.B}")
 
     def run(self, max_new_tokens) -> RolloutResult:
         """Generates up to max_new_tokens[b] tokens per sequence (or until eos)
@@ -59,7 +80,8 @@ class Rollout:
         ones returned for it (those after its eos or past its limit).  A
         finished sequence's automaton is not used again by this rollout; a
         caller that goes on with it should reset and rebuild it from the
-        returned text."""
+        returned text.  With a cache, a finished sequence's row is emptied and
+        its pages are given back."""
         dev = self.batch.device
         B = self.batch.B
         limit = [int(x) for x in max_new_tokens]
@@ -78,12 +100,22 @@ class Rollout:
         # outputs the host reads (emit, emit_len, status, accept_len), so that
         # a step costs one device-to-host copy
         ws = verify_workspace(len(active), self.K, 1, dev)
-        hostbuf = torch.empty(len(active) * (self.K + 4), dtype=torch.int32, device=dev)
+        hostbuf = torch.empty(len(active) * (self.K + 5), dtype=torch.int32, device=dev)
+        cache, plan_status = self.cache, None
+        if cache is not None:
+            last = self.last[rows.long()]
+            group = self.group[rows.long()] if self.group is not None else None
         step = 0
         while active:
             n = len(active)
             n_done = torch.tensor([len(out[b]) for b in active], dtype=torch.int64, device=dev)
-            logits = self.model(rows, n_done, draft, dlen)
+            if cache is None:
+                logits = self.model(rows, n_done, draft, dlen)
+            else:
+                n_tok = dlen + 1
+                cache.reserve(rows, n_tok)   # what it refuses, the plan refuses
+                plan = cache.plan(int(draft.shape[1]) + 1, self.q_heads, rows=rows, n_tok=n_tok, group=group)
+                logits = self.model(rows, n_done, torch.cat((last[:, None], draft), 1), n_tok, plan)
             k_next = speculation_k(n, self.threshold, self.K)
             K1 = int(draft.shape[1]) + 1
             o = {"emit": hostbuf[:n * K1].view(n, K1), "emit_len": hostbuf[n * K1:n * K1 + n],
@@ -94,13 +126,23 @@ class Rollout:
                                      workspace=ws, out=o)
             res.k_per_step.append(int(draft.shape[1]))
             res.active_per_step.append(n)
-            h = hostbuf[:n * K1 + 3 * n].cpu()
+            read = n * K1 + 3 * n
+            if cache is not None:
+                last = r["out_token"]
+                cache.commit(rows, r["accept_len"])
+                hostbuf[read:read + n] = plan.status
+                read += n
+            h = hostbuf[:read].cpu()
+            if cache is not None:
+                plan_status = h[n * K1 + 3 * n:].tolist()
             emit = h[:n * K1].view(n, K1).tolist()
             elen = h[n * K1:n * K1 + n].tolist()
             st = h[n * K1 + n:n * K1 + 2 * n].tolist()
             acc = h[n * K1 + 2 * n:n * K1 + 3 * n].tolist()
             keep = []
             for i, b in enumerate(active):
+                if plan_status is not None and plan_status[i] != 0:
+                    raise RuntimeError(f"sequence {b}: cache status {plan_status[i]}")
                 if st[i] != 0:
                     raise RuntimeError(f"sequence {b}: verification status {st[i]}")
                 res.accepted += acc[i]
@@ -118,6 +160,12 @@ class Rollout:
             res.steps = step
             if len(keep) != n:
                 idx = torch.tensor(keep, dtype=torch.int64, device=dev)
+                if cache is not None:
+                    kept = set(keep)
+                    cache.truncate(torch.tensor([b for i, b in enumerate(active) if i not in kept],
+                                                dtype=torch.int32, device=dev))
+                    last = last[idx].contiguous()
+                    group = group[idx].contiguous() if group is not None else None
                 active = [active[i] for i in keep]
                 rows = rows[idx].contiguous()
                 draft = r["next_draft"][idx].contiguous()
