@@ -510,9 +510,10 @@ __device__ __forceinline__ uint64_t desc(uint32_t low) {
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, uint64_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
-  for (uint32_t k = limit < 1000000 ? 0 : 1;; ++k) {
+  const uint32_t mask = limit < 1000000 ? 0 : 255;  // (short limits are a test's)
+  for (uint32_t k = 1;; ++k) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (k & 255) continue;
+    if (k & mask) continue;
     if (vload(&ctl->abort)) return false;
     const uint64_t t = global_ns();
     if (t0 == 0) t0 = t;

@@ -1,0 +1,253 @@
+"""The paged cache without a GPU: exported symbols, arguments that the C entry
+points refuse before any launch (placeholder pointers, never touched), the
+binding's own checks, and the frequency tables."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import sam_drafting_verification_gb300 as ss
+from sam_drafting_verification_gb300 import _binding as bd
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 4096   # an aligned address
+
+
+def test_library_exports_every_declared_symbol():
+    src = open(os.path.join(ROOT, "include", "samspec_kv.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = sorted(set(re.findall(r"\b(kv_[a-z_]+)\s*\(", src)))
+    assert names == sorted(bd.KV_EXPORTED)
+    lib = bd.lib()
+    assert all(hasattr(lib, n) for n in names)
+
+
+def test_status_words_have_texts():
+    lib = bd.lib()
+    src = open(os.path.join(ROOT, "include", "samspec_kv.h")).read()
+    codes = {m[0]: int(m[1]) for m in re.findall(r"#define\s+(SAMSPEC_ST_[A-Z]+)\s+(\d+)", src)}
+    assert codes == {"SAMSPEC_ST_PAGE": bd.ST_PAGE, "SAMSPEC_ST_ROW": bd.ST_ROW}
+    texts = [lib.samspec_strerror(v) for v in range(0, 12)]
+    assert len(set(texts)) == 12 and b"unknown code" not in texts
+
+
+def desc(**kw):
+    f = dict(k=P, v=P, table=P, lens=P, held=P, refs=P, free_bits=P, dtype=bd.BF16, layers=2, n_pages=100, page=64,
+             kv_heads=4, head_dim=128, seqs=8, max_pages=10)
+    f.update(kw)
+    return ctypes.byref(bd.KvCacheDesc(*f.values()))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=0), bd.EINVAL), (dict(table=0), bd.EINVAL), (dict(free_bits=0), bd.EINVAL),
+    (dict(dtype=bd.F32), bd.EDTYPE), (dict(dtype=9), bd.EDTYPE),
+    (dict(page=8), bd.ESIZE), (dict(page=48), bd.ESIZE), (dict(page=256), bd.ESIZE), (dict(head_dim=96), bd.ESIZE),
+    (dict(kv_heads=0), bd.ESIZE), (dict(kv_heads=1025), bd.ESIZE), (dict(layers=0), bd.ESIZE), (dict(seqs=0), bd.ESIZE),
+    (dict(max_pages=0), bd.ESIZE), (dict(max_pages=(1 << 20) + 1), bd.ESIZE), (dict(n_pages=1 << 30, layers=2), bd.ESIZE),
+    (dict(n_pages=1 << 24, kv_heads=8, page=16), bd.ESIZE), (dict(k=P + 8), bd.EALIGN), (dict(v=P + 4), bd.EALIGN),
+])
+def test_every_entry_point_refuses_a_bad_cache(kw, code):
+    lib, d = bd.lib(), desc(**kw)
+    assert lib.kv_reserve(d, None, 2, 4, None, None, P, 1 << 20, None) == code
+    assert lib.kv_fork(d, P, P, 2, None, None) == code
+    assert lib.kv_commit(d, None, 2, 4, P, None, None, None) == code
+    assert lib.kv_truncate(d, None, 2, None, None, None) == code
+    assert lib.kv_plan(d, None, 2, 4, 8, None, None, None, None, P, 1 << 30, None) == code
+    assert lib.kv_append(d, 0, P, 2, 4, 8, None, 0, None, P, 512, P, 512, None, 0, 0, 1.0, None) == code
+    assert lib.kv_attend(d, 0, P, 1 << 30, 2, 4, 8, P, 1024, 0.1, P, None) == code
+    assert lib.kv_plan_bytes(d, 2, 4, 8, 0) == 0 and lib.kv_reserve_workspace_bytes(d, 2) == 0
+
+
+def test_a_null_cache_is_refused():
+    lib = bd.lib()
+    assert lib.kv_truncate(None, None, 2, None, None, None) == bd.EINVAL
+    assert lib.kv_plan_bytes(None, 2, 4, 8, 0) == 0
+
+
+def test_page_calls_refuse_bad_arguments():
+    lib, d = bd.lib(), desc()
+    need = lib.kv_reserve_workspace_bytes(d, 3)
+    assert need > 0
+
+    def reserve(rows=P, n=3, N=4, ws=P, size=need):
+        return lib.kv_reserve(d, rows, n, N, None, None, ws, size, None)
+
+    assert reserve(ws=None) == bd.EINVAL and reserve(n=0) == bd.ESIZE and reserve(N=-1) == bd.ESIZE
+    assert reserve(size=need - 1) == bd.ESIZE and reserve(ws=P + 8) == bd.EALIGN
+    assert reserve(rows=None, n=9) == bd.ESIZE      # more than the cache has
+    assert lib.kv_fork(d, None, P, 2, None, None) == bd.EINVAL and lib.kv_fork(d, P, P, 0, None, None) == bd.ESIZE
+    assert lib.kv_commit(d, P, 2, 4, None, None, None, None) == bd.EINVAL
+    assert lib.kv_commit(d, P, 2, 33, P, P, P, None) == bd.ESIZE    # paths of 32 nodes at most
+    assert lib.kv_commit(d, P, 2, 4, P, P, None, None) == bd.EINVAL  # a path needs the status
+    assert lib.kv_commit(d, None, 9, 4, P, None, None, None) == bd.ESIZE
+    assert lib.kv_truncate(d, None, 9, None, None, None) == bd.ESIZE
+    assert lib.kv_truncate(d, P, 0, None, None, None) == bd.ESIZE
+
+
+def test_plan_refuses_bad_arguments():
+    lib, d = bd.lib(), desc()
+    small, large = (lib.kv_plan_bytes(d, 3, 4, 8, g) for g in (0, 1))
+    assert 0 < small < large
+
+    def plan(n=3, N=4, q=8, fc=None, ns=None, group=None, buf=P, size=large):
+        return lib.kv_plan(d, P, n, N, q, None, fc, ns, group, buf, size, None)
+
+    assert plan(buf=None) == bd.EINVAL and plan(fc=P) == bd.EINVAL and plan(ns=P) == bd.EINVAL
+    assert plan(size=small - 1) == bd.ESIZE and plan(group=P, size=small) == bd.ESIZE and plan(buf=P + 16) == bd.EALIGN
+    assert plan(N=33, fc=P, ns=P, size=1 << 40) == bd.ESIZE
+    for n, N, q in ((0, 4, 8), (3, 0, 8), (3, 4, 0), (3, 4, 6), (3, 4, 4 * 65), (3, (1 << 16) + 1, 8),
+                    ((1 << 20) + 1, 1, 4), (1 << 14, 1 << 14, 4)):
+        assert lib.kv_plan_bytes(d, n, N, q, 0) == 0 and plan(n=n, N=N, q=q, size=1 << 60) == bd.ESIZE
+
+
+def test_append_and_attend_refuse_bad_arguments():
+    lib, d = bd.lib(), desc()
+    size = lib.kv_plan_bytes(d, 3, 4, 8, 0)
+
+    def append(layer=0, plan=P, q=P, qs=1024, qo=P, k=P, ks=512, v=P, vs=512, freq=P, rot=128, layout=0):
+        return lib.kv_append(d, layer, plan, 3, 4, 8, q, qs, qo, k, ks, v, vs, freq, rot, layout, 1.0, None)
+
+    assert append(layer=2) == bd.EINVAL and append(layer=-1) == bd.EINVAL and append(plan=None) == bd.EINVAL
+    assert append(k=None) == bd.EINVAL and append(v=None) == bd.EINVAL and append(qo=None) == bd.EINVAL
+    assert append(q=None) == bd.EINVAL and append(freq=None) == bd.EINVAL and append(layout=2) == bd.EINVAL
+    assert append(rot=130) == bd.ESIZE and append(rot=3) == bd.ESIZE and append(rot=-2) == bd.ESIZE
+    assert append(ks=504) == bd.EINVAL and append(vs=0) == bd.EINVAL and append(qs=1016) == bd.EINVAL
+    assert append(ks=516) == bd.EALIGN and append(qs=1025, qo=P + 16384) == bd.EALIGN and append(k=P + 2) == bd.EALIGN
+    assert append(qs=1536) == bd.EINVAL          # in place only where tokens follow one another
+    assert append(plan=P + 64) == bd.EALIGN
+
+    def attend(layer=0, plan=P, bytes=size, q=P, qs=1024, scale=0.1, out=P):
+        return lib.kv_attend(d, layer, plan, bytes, 3, 4, 8, q, qs, scale, out, None)
+
+    assert attend(layer=2) == bd.EINVAL and attend(plan=None) == bd.EINVAL and attend(q=None) == bd.EINVAL
+    assert attend(out=None) == bd.EINVAL
+    for s in (0.0, -0.1, math.nan, math.inf):
+        assert attend(scale=s) == bd.EINVAL
+    assert attend(bytes=size - 1) == bd.ESIZE and attend(qs=1016) == bd.EINVAL and attend(qs=1028) == bd.EALIGN
+    assert attend(q=P + 8) == bd.EALIGN and attend(out=P + 2) == bd.EALIGN and attend(plan=P + 128) == bd.EALIGN
+
+
+# ------------------------------------------------------------- the binding ----
+
+class _Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 4096 if name.endswith("_bytes") else 0
+        return entry
+
+
+@pytest.fixture
+def cache(monkeypatch):
+    rec = _Recorder()
+    monkeypatch.setattr(bd, "lib", lambda: rec)
+    monkeypatch.setattr(ss, "_is_cuda", lambda t: t.device.type in ("cpu", "meta"))
+    monkeypatch.setattr(ss, "_stream", lambda device=None: None)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros((2, 5, 2, 16, 64), dtype=torch.bfloat16)
+    c = ss.KVCache.wrap(k, k.clone(), i(4, 3), i(4), i(4), i(5), i(1))
+    c.rec = rec
+    return c
+
+
+def i32(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+def names(c):
+    return [n for n, _ in c.rec.calls if not n.endswith("_bytes")]
+
+
+def test_wrap_checks_every_tensor(cache):
+    i = i32
+    k = torch.zeros((2, 5, 2, 16, 64), dtype=torch.bfloat16)
+    good = [k, k, i(4, 3), i(4), i(4), i(5), i(1)]
+    for at, bad, err in ((0, k.float(), TypeError), (0, k[0], ValueError), (1, k.half(), TypeError), (1, k[:1], ValueError),
+                         (1, k.transpose(2, 3), ValueError), (2, i(12), ValueError), (2, i(4, 3).long(), TypeError),
+                         (3, i(5), ValueError), (4, i(3), ValueError), (5, i(4), ValueError), (6, i(2), ValueError),
+                         (3, torch.zeros(4, dtype=torch.int32, device="meta"), ValueError), (0, None, TypeError)):
+        args = list(good)
+        args[at] = bad
+        with pytest.raises(err):
+            ss.KVCache.wrap(*args)
+
+
+def test_page_calls_check_their_tensors(cache):
+    c = cache
+    assert c.reserve(i32(2), i32(2)).shape == (2,) and c.reserve(None, 7).shape == (4,)
+    assert c.truncate(i32(3)).shape == (3,) and c.commit(i32(2), i32(2), i32(2, 8)).shape == (2,)
+    assert c.fork(i32(2), i32(2)).shape == (2,)
+    assert names(c) == ["kv_reserve"] * 2 + ["kv_truncate", "kv_commit", "kv_fork"]
+    c.rec.calls.clear()
+    for call in (lambda: c.reserve(i32(2), i32(3)), lambda: c.reserve(i32(2).long(), i32(2)), lambda: c.reserve(i32(2, 1), 1),
+                 lambda: c.reserve(i32(4)[::2], i32(2)), lambda: c.reserve(None, i32(9)), lambda: c.reserve([0], 1),
+                 lambda: c.commit(i32(2), i32(3)), lambda: c.commit(i32(2), i32(2), i32(3, 8)), lambda: c.commit(i32(2), 3),
+                 lambda: c.commit(i32(2), i32(2), i32(2)), lambda: c.fork(i32(2), i32(1)), lambda: c.fork(None, i32(1)),
+                 lambda: c.truncate(i32(2), i32(1)), lambda: c.truncate(i32(2), i32(2), out=i32(3)),
+                 lambda: c.truncate(i32(2), torch.zeros(2)), lambda: c.truncate(None, i32(6))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    assert names(c) == []
+
+
+def test_passes_check_their_tensors(cache):
+    c = cache
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    plan = c.plan(3, 4, rows=i32(2), n_tok=i32(2))
+    assert plan.status.shape == (2,)
+    wide = bf(2, 3, 8, 64)
+    out = c.attend(1, plan, wide[:, :, 2:6])
+    assert out.shape == (2, 3, 4, 64) and out.is_contiguous()
+    assert c.append(0, plan, wide[:, :, :4], wide[:, :, 4:6], wide[:, :, 6:]).shape == (2, 3, 4, 64)
+    assert c.append(0, plan, None, bf(2, 3, 2, 64), bf(2, 3, 2, 64)) is None
+    strides = [a for n, a in c.rec.calls if n == "kv_append"][0]
+    assert strides[7] == 512 and strides[10] == 512
+    assert names(c) == ["kv_plan", "kv_attend", "kv_append", "kv_append"]
+    c.rec.calls.clear()
+    q, k = bf(2, 3, 4, 64), bf(2, 3, 2, 64)
+    for call in (lambda: c.plan(3, 4, rows=i32(2), n_tok=i32(3)), lambda: c.plan(3, 4, tree=(i32(4, 3), i32(4, 2))),
+                 lambda: c.plan(3, 4, rows=i32(2), group=i32(4)), lambda: c.plan(2, 4, rows=i32(2), out=plan),
+                 lambda: c.plan(3, 4, rows=i32(2), group=i32(2), out=plan),
+                 lambda: c.attend(0, plan, q.half()), lambda: c.attend(0, plan, bf(2, 3, 5, 64)), lambda: c.attend(0, plan, None),
+                 lambda: c.attend(0, plan, bf(2, 3, 4, 128)[..., ::2]), lambda: c.attend(0, plan, bf(2, 4, 4, 64)[:, :3]),
+                 lambda: c.attend(0, plan, bf(2, 4, 3, 64).transpose(1, 2)), lambda: c.attend(0, plan, q, out=bf(2, 3, 4, 32)),
+                 lambda: c.append(0, plan, q, bf(2, 3, 4, 64), k), lambda: c.append(0, plan, q, k, k.float()),
+                 lambda: c.append(0, plan, q, k, k, ss.Rope(torch.zeros(33, dtype=torch.float64))),
+                 lambda: c.append(0, plan, q, k, k, out=q.float())):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    assert names(c) == []
+
+
+def test_rope_refuses_what_it_cannot_turn(cache):
+    for f, layout, m in ((torch.zeros(4), "half", 1.0), (torch.zeros((2, 2), dtype=torch.float64), "half", 1.0),
+                         (torch.zeros(0, dtype=torch.float64), "half", 1.0),
+                         (torch.zeros(4, dtype=torch.float64), "quarter", 1.0),
+                         (torch.zeros(4, dtype=torch.float64), "half", math.nan)):
+        with pytest.raises((TypeError, ValueError)):
+            ss.Rope(f, layout, m)
+
+
+def test_frequencies():
+    f, m = ss.rope_frequencies(8, base=100.0)
+    assert m == 1.0 and torch.allclose(f, torch.tensor([1.0, 100 ** -0.25, 0.1, 100 ** -0.75], dtype=torch.float64))
+    g, _ = ss.rope_frequencies(8, base=100.0, scaling="linear", factor=4.0)
+    assert torch.allclose(g, f / 4)
+    n, _ = ss.rope_frequencies(8, base=100.0, scaling="ntk", factor=4.0)
+    assert math.isclose(float(n[0]), 1.0) and math.isclose(float(n[-1]), float(f[-1]) / 4)
+    y, m = ss.rope_frequencies(64, scaling="yarn", factor=8.0, original_len=2048)
+    f, _ = ss.rope_frequencies(64)
+    assert math.isclose(m, 0.1 * math.log(8) + 1)
+    turns = 2048 * f / (2 * math.pi)
+    # pairs that turn often are kept, those that turn less than once are stretched, none is outside
+    assert torch.equal(y[turns > 64], f[turns > 64]) and torch.allclose(y[turns < 0.5], f[turns < 0.5] / 8)
+    assert ((y <= f) & (y >= f / 8 * (1 - 1e-12))).all()
+    for bad in (dict(rot=3), dict(rot=0), dict(rot=8, scaling="other"), dict(rot=8, base=-1.0), dict(rot=8, factor=0.0)):
+        with pytest.raises(ValueError):
+            ss.rope_frequencies(**bad)
