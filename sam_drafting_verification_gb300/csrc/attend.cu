@@ -161,11 +161,15 @@ __global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
 // One CTA: what a group reads once, the units of work and their order, and
 // each persistent CTA's equal share of the key blocks.
 constexpr int kMinShared = 128;  // tokens: less is read by each sequence for itself
-// Costs, in blocks of a unit of one row tile (2600 clocks, by HBM): a block of
-// two row tiles (two steps of softmax on each warp), and what a unit costs
-// besides its blocks (the start and end of its two streams).
-constexpr int kUnitCost = 4;
-__device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? 2 : 1; }
+// Costs, in blocks of a unit of one row tile (2800 clocks, by HBM): a block of
+// two row tiles, and what a unit costs besides its blocks (the start and end of
+// its streams; more where its results are partial, in fp32, or two tiles').
+// Measured: 256 trees over short histories 52 us with 4 for every unit and 46
+// with 2; groups of 16 with 880 own keys each 437 us with 2 and 418 with 4;
+// prompt chunks 148 us with 2 and 119 with 4.
+constexpr int kBlockCost2 = 2;
+__device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? kBlockCost2 : 1; }
+__device__ __forceinline__ int unit_cost(const KvTile& t) { return t.two || t.kind ? 4 : 2; }
 
 __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __shared__ int part[32];
@@ -243,14 +247,15 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   for (int t0 = 0; t0 < tiles; t0 += 1024) {
     const int t = t0 + tid;
     int sum;
-    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks * block_cost(P.plan.tile[t]) + kUnitCost) * c.kv_heads : 0,
+    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks * block_cost(P.plan.tile[t]) +
+                                           unit_cost(P.plan.tile[t])) * c.kv_heads : 0,
                               part, &sum);
     if (t < tiles) P.plan.tile[t].cost0 = cost + at;
     cost += sum;
   }
   __syncthreads();
-  // costs of at least 2 lie between two shares: no two begin in one block
-  const int ctas = min(kKvCtas, (cost + 1) / 2);
+  // at least a block's cost lies between two shares, so no two begin in one block
+  const int ctas = cost ? min(kKvCtas, max(1, cost / kBlockCost2)) : 0;
   for (int x = tid; x <= ctas; x += 1024) {
     const int b = ctas ? (int)((int64_t)x * cost / ctas) : 0;
     int lo = 0, hi = tiles - 1;  // the last tile that begins at or before b
@@ -264,11 +269,10 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
     int4 s = {tiles, 0, 0, 0};
     if (x < ctas) {
       const KvTile t = P.plan.tile[lo];
-      const int bc = block_cost(t), u = t.blocks * bc + kUnitCost;
+      const int bc = block_cost(t), uc = unit_cost(t), u = t.blocks * bc + uc;
       s.x = lo;
       s.y = (b - t.cost0) / u;
-      s.z = ((b - t.cost0) % u - kUnitCost + bc - 1) / bc;
-      if (s.z < 0) s.z = 0;
+      s.z = max(((b - t.cost0) % u - uc + bc - 1) / bc, 0);
       if (s.z == t.blocks) {  // behind the unit's last block
         s.z = 0;
         if (++s.y == c.kv_heads) {
@@ -1117,8 +1121,8 @@ __global__ void __launch_bounds__(384, 1)
 // The CTAs [c0, c1] that hold the blocks of unit (tile t, head h): those of its
 // first and its last block, each the last that begins at or before it.
 __device__ __forceinline__ int2 unit_ctas(const KvTile& t, int h, int ctas, int cost) {
-  const int bc = block_cost(t);
-  const int64_t b0 = t.cost0 + h * (t.blocks * bc + kUnitCost) + kUnitCost + 1;
+  const int bc = block_cost(t), uc = unit_cost(t);
+  const int64_t b0 = t.cost0 + h * (t.blocks * bc + uc) + uc + 1;
   return {(int)((b0 * ctas - 1) / cost), (int)(((b0 + (t.blocks - 1) * bc) * ctas - 1) / cost)};
 }
 // Row `at` of a cut unit: where its part of CTA c0 lies (that one's first

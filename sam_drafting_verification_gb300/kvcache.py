@@ -156,7 +156,6 @@ class KVCache:
                                                                          seqs, max_pages)))
         self._ref = ctypes.byref(self._desc)
         self._bytes = {}   # workspace sizes by call sizes
-        self._byte = torch.empty(0, dtype=torch.uint8, device=dev)
 
     # -- helpers ---------------------------------------------------------------
     def _call(self, name, *args):
@@ -196,7 +195,7 @@ class KVCache:
 
     def _status(self, n, out):
         if out is None:
-            return self.lens.new_empty(n)
+            return torch.empty(n, dtype=torch.int32, device=self.device)
         self._i32(out, "out", (n,))
         return out
 
@@ -217,7 +216,7 @@ class KVCache:
         need = self._bytes.get(n)
         if need is None:
             need = self._bytes[n] = int(self.lib.kv_reserve_workspace_bytes(self._ref, n))
-        ws = self._byte.new_empty(need)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         self._call("kv_reserve", rp, n, most, np, st.data_ptr(), ws.data_ptr(), need)
         return st
 
@@ -290,7 +289,7 @@ class KVCache:
                 need = self._bytes[key] = int(self.lib.kv_plan_bytes(self._ref, n, N, q_heads, gp is not None))
             if need == 0:
                 raise _b.SamspecError(f"sizes outside the limits: n={n}, N={N}, q_heads={q_heads}")
-            out = KVPlan(n, N, q_heads, gp is not None, self._byte.new_empty(need))
+            out = KVPlan(n, N, q_heads, gp is not None, torch.empty(need, dtype=torch.uint8, device=self.device))
         elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.buf.device != self.device or \
                 (gp is not None and not out.grouped):
             raise ValueError("out: a plan of other sizes")
@@ -318,7 +317,7 @@ class KVCache:
     def _output(self, out, plan):
         shape = (plan.n, plan.N, plan.q_heads, self.head_dim)
         if out is None:
-            return self.k.new_empty(shape)
+            return torch.empty(shape, dtype=self.dtype, device=self.device)
         return _req(out, self.dtype, "out", shape, self.device)
 
     def append(self, layer: int, plan: KVPlan, q, k, v, rope: Rope | None = None, out=None):
