@@ -47,8 +47,8 @@ extern "C" {
  * n_pages, and any table.  Sequences that share pages (kv_fork) never write
  * to them: kv_reserve copies a shared page before it is appended to.
  * Limits: page 16, 32, 64 or 128; head_dim 64 or 128; 1 <= kv_heads <= 1024;
- * 1 <= layers; seqs, max_pages <= 2^20; n_pages * layers, n_pages * kv_heads *
- * page and max_pages * page < 2^31.
+ * 1 <= layers; seqs, max_pages <= 2^20; max_pages * page < 2^30; n_pages *
+ * layers and n_pages * kv_heads * page < 2^31.
  *
  * Calls name n sequences by d_rows [n] (NULL: 0 .. n-1), each at most once;
  * d_status [n] (may be NULL) receives ST_OK or why a sequence was left as it
@@ -119,9 +119,11 @@ int kv_truncate(const kv_cache* cache, const int32_t* d_rows, int32_t n,
  * aligned, any content; it starts with the n status words, and holds the
  * workspace of kv_attend: one kv_attend at a time may use a plan (grouped:
  * non-zero where d_group is given, which takes more of it).  kv_attend is
- * given the same plan_bytes, n, N and q_heads as kv_plan.  A plan holds until the cache's lengths or tables change.  Limits: n <= 2^20,
- * N <= 2^16, q_heads a multiple of kv_heads, at most 64 times as many,
- * n * N * q_heads < 2^30. */
+ * given the same plan_bytes, n, N and q_heads as kv_plan.  A plan holds until
+ * the cache's lengths or tables change.  Limits: n <= 2^20, N <= 2^16, q_heads
+ * a multiple of kv_heads, at most 64 times as many, n * N * q_heads < 2^30
+ * (with groups 2^29), and units of work times key blocks below 2^31 (a call
+ * of some 2000 sequences of a million tokens each and 8 key heads). */
 size_t kv_plan_bytes(const kv_cache* cache, int32_t n, int32_t N, int32_t q_heads,
                      int32_t grouped);
 int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, int32_t q_heads,

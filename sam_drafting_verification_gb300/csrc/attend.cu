@@ -653,6 +653,7 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
   for (int key = from; key < to; ++key) {
     if (!(key < lim || (key >= base && key - base < 32 && ((see >> (key - base)) & 1)))) continue;
     const int pg = c.table[(int64_t)seq_row * c.max_pages + (key >> c.log_page)];
+    if (pg < 0 || pg >= c.n_pages) continue;
     const uint32_t* v = reinterpret_cast<const uint32_t*>(
         c.v + kv_offset(c, P.layer, pg, head) + ((int64_t)(key & (c.page - 1)) * c.head_dim + d0) * 2);
 #pragma unroll 1
@@ -672,10 +673,7 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
 }
 
 // One persistent CTA an SM.  Warp 8 loads queries and pages by TMA, warp 9
-// issues matrix products, two warpgroups do the softmax, a thread a row.  (What
-// is spilled goes to L2, since shared memory leaves no L1: a thread holds a
-// row's 128 scores in registers.  Two warpgroups a stream of 64 keys each have
-// 104 registers a thread and read the scores twice: ...)
+// issues matrix products, two warpgroups do the softmax, a thread a row.
 //
 // A step is one block of 128 keys against 128 query rows: S = Q K^T (both in
 // shared memory, S in tensor memory), P = exp2(S - m) rounded to 16 bits over
@@ -689,9 +687,26 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
 // so the next segment's first scores are computed while this one's last are
 // worked on; only its first product into O waits until O has been read.
 //
-// Few rows (a decode step has N * rep of 128) waste the matrix unit but not
-// memory time: at 128 keys * D * 4 bytes a step HBM takes about 2800 clocks an
-// SM, the two products 1024, a warp's softmax about 1500 with two in flight.
+// P is rounded to the cache's type, as the product takes it: half a step of
+// each weight, which the 64-bit tests' bounds count; sums, maxima and O stay in
+// fp32.
+//
+// What bounds it.  One tile of rows: HBM.  A block is 128 keys * D * 4 bytes,
+// 2800 clocks of an SM's share, against 1090 for the two products and 1500 for
+// a warp's softmax with two in flight; few rows (a decode step has N * rep of
+// 128) waste the matrix unit but no time.  16 sequences of 32768 keys, 8 key
+// heads of 128, 32 rows each: 322 us, 6.7 TB/s of 6.8.  Two tiles: a step of
+// each stream takes 2000 clocks, half of it the matrix unit (1130 TFLOP/s over
+// 32768 keys); what is left is the chain S, softmax, P, product, S of a stream,
+// of which the softmax is 1470 (reading S 340, maximum 150, exponentials 750).
+// A unit's start and end cost about 5000 clocks.
+//
+// Registers decide that chain.  What is spilled goes to L2, since shared memory
+// leaves no L1: 100 bytes a thread cost 5%, 300 bytes twice the time.  So a
+// thread holds a row's 128 scores (216 registers), and the sums are read 16
+// columns at a time.  Two warpgroups a stream with 64 keys each (104 registers)
+// had to read the scores twice, and took 256 us where this takes 241; giving
+// the product its first 64 keys early took 252; spinning instead of waiting 270.
 template <typename T, int D>
 __global__ void __launch_bounds__(384, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,
@@ -882,12 +897,14 @@ __global__ void __launch_bounds__(384, 1)
     int g0 = 0, kb = 0, qt = 0, seg = 0;  // steps, blocks, query tiles and segments before
     bool last = !Walk(P).more();
     bool ok = true;
-    for (; !last; ++seg) {
-      ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
-      if (named_any(4, 256, !ok)) {
-        ok = false;
-        break;
-      }
+    // a segment has come: all threads of both streams decide alike whether to
+    // go on, and are done with the last one's exchange and flag
+    auto next_segment = [&](int q) {
+      const bool came = wait_for(&ctl->q_full[q & 1], (q >> 1) & 1, ctl, P.wait_ns);
+      return !named_any(4, 256, !came);
+    };
+    if (!last) ok = next_segment(0);
+    for (; ok && !last; ++seg) {
       const Segment& sg = ctl->seg[seg & 3];  // the loader is two segments ahead at most
       const bool rows2 = sg.t.two;
       const int items = rows2 ? 2 * sg.nb : sg.nb;
@@ -1093,12 +1110,18 @@ __global__ void __launch_bounds__(384, 1)
                        direct ? P.out + (q_row * D + d0) * 2 : nullptr, P.plan.o + slot * D + d0);
       if (live && !direct && (rows2 || w == 0)) P.plan.ml[slot] = {m == -INFINITY ? m : m * sc, l};
       last = sg.last;
-      // the exchange and the flag may be used again
-      named_sync(4, 256);
-      if (bad && tid == 0) ctl->bad = 0;
       g0 += items;
       kb += nb;
       qt += rows2 ? 2 : 1;
+      if (!last) {
+        ok = next_segment(qt);
+        if (!ok) ++seg;
+        if (bad) {  // (rare: the flag is cleared between two barriers)
+          if (tid == 0) ctl->bad = 0;
+          named_sync(4, 256);
+        }
+      }
+      if (!ok) break;
     }
     if (!ok) {
       // the sequences of this and the following units have no result
@@ -1391,7 +1414,8 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   AttendParams P;
   const int rc = kv_view(cache, &P.c);
   if (rc != SAMSPEC_OK) return rc;
-  if (!d_plan || !d_q || !d_out || layer < 0 || layer >= P.c.layers || !std::isfinite(scale) || !(scale > 0))
+  if (!d_plan || !d_q || !d_out || layer < 0 || layer >= P.c.layers || !(scale > 0) ||
+      !std::isfinite(scale * 1.4426950408889634f))
     return SAMSPEC_EINVAL;
   PlanLayout l;
   if (!plan_of(P.c, n, N, q_heads, plan_bytes, &l)) return SAMSPEC_ESIZE;

@@ -510,11 +510,14 @@ __global__ void __launch_bounds__(256, 2) append_kernel(AppendParams P) {
     const int k0 = c.kv_heads * part / P.parts, k1 = c.kv_heads * (part + 1) / P.parts;
     const KvSeq& s = P.plan.seq[i];
     unsigned char* q_out = P.q_out + (int64_t)tok * P.q_heads * D * 2;
-    if (node >= s.ntok) {
+    // (the page was checked when the pass was planned; a plan used after the
+    // table has changed must not write outside the pool)
+    const int z = s.base + node;
+    const int page = node < s.ntok ? c.table[(int64_t)s.row * c.max_pages + (z >> c.log_page)] : -1;
+    if (page < 0 || page >= c.n_pages) {
       for (int x = q0 * kVec + lane; x < q1 * kVec; x += 32) reinterpret_cast<uint4*>(q_out)[x] = uint4{0, 0, 0, 0};
       continue;
     }
-    const int z = s.base + node, page = c.table[(int64_t)s.row * c.max_pages + (z >> c.log_page)];
     const int64_t at = kv_offset(c, P.layer, page, 0) + (int64_t)(z & (c.page - 1)) * D * 2;
     const int64_t pos = (int64_t)s.base + (tree ? P.plan.node[tok].x : node);
     const unsigned char* q = P.q + (int64_t)tok * P.q_stride * 2;

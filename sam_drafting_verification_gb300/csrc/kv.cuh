@@ -42,7 +42,7 @@ inline int kv_view(const kv_cache* c, KvView* o) {
     return SAMSPEC_ESIZE;
   const int64_t lim = (int64_t)1 << 31;
   if ((int64_t)c->layers * c->n_pages >= lim || (int64_t)c->n_pages * c->kv_heads * c->page >= lim ||
-      (int64_t)c->max_pages * c->page >= lim)
+      (int64_t)c->max_pages * c->page >= lim / 2)
     return SAMSPEC_ESIZE;
   if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) % 16 != 0)
     return SAMSPEC_EALIGN;
@@ -149,7 +149,7 @@ inline size_t kv_align(size_t x) { return (x + 255) / 256 * 256; }
 inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_heads, bool grouped) {
   PlanLayout p = {};
   if (n < 1 || n > (1 << 20) || N < 1 || N > (1 << 16) || q_heads < 1 || q_heads % c.kv_heads != 0 ||
-      q_heads / c.kv_heads > 64 || (int64_t)n * N * q_heads >= ((int64_t)1 << 30))
+      q_heads / c.kv_heads > 64 || (int64_t)n * N * q_heads >= ((int64_t)1 << (grouped ? 29 : 30)))
     return p;
   const int64_t rep = q_heads / c.kv_heads;
   const int64_t unit = 2 * tile_tokens((int)rep);  // tokens

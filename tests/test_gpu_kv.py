@@ -128,6 +128,83 @@ def test_attend_trees(ss, cuda_device, N, Q, H, page, D):
     check_attend(c, table, q, out, LENS, [N] * n, parent)
 
 
+@pytest.mark.parametrize("seed", range(5))
+def test_attend_many_small_shapes(ss, cuda_device, seed):
+    """Few blocks, odd head counts and lengths: shares of single blocks, units cut
+    in two and three, tiles of whole tokens that leave rows over."""
+    rng = np.random.default_rng(seed)
+    for _ in range(14):
+        n, rep = int(rng.integers(1, 5)), int(rng.choice([1, 2, 3, 5, 7, 8, 20, 43, 48, 64]))
+        H, page, D = int(rng.choice([1, 1, 2, 3])), int(rng.choice([16, 32, 64, 128])), int(rng.choice([64, 128]))
+        N = int(rng.integers(1, 1 + max(1, 600 // rep)))
+        lens = [int(x) for x in rng.integers(0, int(rng.choice([2, 100, 700])), n)]
+        n_tok = [int(x) for x in rng.integers(0, N + 1, n)]
+        n_tok[0] = N
+        c, table = make(ss, cuda_device, lens, n_tok, page, H, D, F16 if rng.random() < 0.5 else BF16, seed=seed)
+        q = queries(n, N, H * rep, D, c.dtype, cuda_device, gain=1.5)
+        plan = c.plan(N, H * rep, n_tok=i32(n_tok, cuda_device))
+        assert (plan.status == 0).all()
+        check_attend(c, table, q, c.attend(0, plan, q), lens, n_tok)
+
+
+def test_a_pool_past_four_gigabytes(ss, cuda_device):
+    """Pages at both ends of pools of 5.6 GB and two layers: append, attend, copy on
+    write and commit all reach them."""
+    dev, page, H, D, N = cuda_device, 128, 8, 128, 5
+    pages = 10_700
+    c = ss.KVCache(2, pages, page, H, D, 3, 4, device=dev)
+    assert c.k.numel() * 2 > 5.6e9
+    # every page but the first and the last few is someone else's
+    c.refs[2:pages - 6] = 1
+    words = torch.zeros(((pages + 31) // 32, 32), dtype=torch.int64)
+    free = torch.zeros(pages, dtype=torch.bool)
+    free[:2], free[pages - 6:] = True, True
+    words.view(-1)[:pages] = free.long()
+    w = (words << torch.arange(32)).sum(1)
+    c.free.copy_(torch.where(w >= 1 << 31, w - (1 << 32), w).int())
+    rows = i32([0], dev)
+    lens = 3 * page - 40
+    assert c.reserve(rows, lens).tolist() == [0]
+    assert c.table[0, :3].tolist() == [0, 1, pages - 6]
+    held = c.table[0, :3].long()
+    for x in (c.k, c.v):
+        x[:, held] = torch.randn((2, 3, H, page, D), generator=torch.Generator(device=dev).manual_seed(1),
+                                 device=dev).to(BF16)
+    c.commit(rows, i32([lens - 1], dev))
+    c.fork(i32([0, 0], dev), i32([1, 2], dev))
+    assert c.reserve(None, N).tolist() == [0, 0, 0]
+    assert sorted(c.table[:, 2].tolist()) == [pages - 5, pages - 4, pages - 3]
+    q, k, v = (queries(3, N, h, D, BF16, dev, seed=s) for s, h in ((1, 16), (2, H), (3, H)))
+    parent = np.array([[-1, 0, 0, 1, 3]] * 3)
+    fc, ns = ref.links(parent)
+    plan = c.plan(N, 16, tree=(i32(fc, dev), i32(ns, dev)), group=i32([0, 0, 0], dev))
+    assert (plan.status == 0).all()
+    c.append(1, plan, None, k, v)
+    table = c.table.cpu().numpy()
+    out = c.attend(1, plan, q)
+    check_attend(c, table, q, out, [lens] * 3, [N] * 3, parent, layer=1)
+    want = torch.cat((gathered(c, table, 1, 2, lens)[1], v[2, [0, 1, 3, 4]]))
+    assert c.commit(None, i32([3, 3, 3], dev), i32([[1, 3, 4, -1, -1]] * 3, dev)).tolist() == [0, 0, 0]
+    assert torch.equal(gathered(c, c.table.cpu().numpy(), 1, 2, lens + 4)[1], want)
+
+
+def test_a_plan_used_too_late_stays_inside_the_pool(ss, cuda_device):
+    """A plan whose sequence was emptied behind its back: what it gives is undefined,
+    but nothing outside the pool is read or written, and nothing of others is."""
+    dev = cuda_device
+    c, table = make(ss, dev, [70, 70], [4, 4], 16, 1, 64)
+    q, k = queries(2, 4, 2, 64, BF16, dev), queries(2, 4, 1, 64, BF16, dev)
+    plan = c.plan(4, 2)
+    c.truncate(i32([0], dev))
+    before = c.k.clone()
+    got = c.append(0, plan, q, k, k)
+    assert (got[0] == 0).all() and torch.equal(got[1], q[1])
+    changed = (before != c.k)[0].flatten(1).any(1).nonzero()[:, 0].tolist()
+    assert set(changed) <= {int(x) for x in table[1]}
+    c.attend(0, plan, q)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("N,Q,H,shared", [(4, 16, 2, 512), (1, 4, 4, 64), (3, 7, 1, 130), (8, 64, 2, 1000)])
 @pytest.mark.parametrize("page", [16, 64])
 def test_attend_groups(ss, cuda_device, N, Q, H, shared, page):
