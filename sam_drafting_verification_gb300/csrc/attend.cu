@@ -172,7 +172,9 @@ __device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? kBlo
 __device__ __forceinline__ int unit_cost(const KvTile& t) { return t.two || t.kind ? 4 : 2; }
 
 __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
+  constexpr int kTilesHere = 8192;
   __shared__ int part[32];
+  __shared__ int costs[kTilesHere];
   const KvView& c = P.c;
   const int tid = threadIdx.x, n = P.n;
   wait_for_previous();
@@ -201,58 +203,57 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
       if (seq[i].leader != i) seq[i].shared = seq[i].ntok > 0 ? seq[seq[i].leader].shared : 0;
     __syncthreads();
   }
-  // tiles of the groups' shared keys, then of each sequence's own
-  int tiles = 0;
-  for (int pass = P.group ? 0 : 1; pass < 2; ++pass)
+  // tiles of the groups' shared keys, then of each sequence's own; the costs
+  // before each are kept in shared memory too, where the shares are looked up
+  auto tile_of = [&](int i, int k, bool own) {
+    KvTile t = {};
+    const int t0 = 2 * tt * k;
+    t.tok0 = i * P.N + t0;
+    t.seq_row = seq[i].row;
+    if (!own) {
+      t.toks = min(2 * tt, seq[i].gsize * P.N - t0);
+      t.kend = t.ctx = seq[i].shared;
+      t.kind = 1;
+    } else {
+      t.toks = min(2 * tt, seq[i].ntok - t0);
+      t.kbeg = seq[i].shared;
+      // a chain's tile sees no further than its last token, and all of it up
+      // to its first; a tree's nodes all see the root
+      t.kend = seq[i].base + (P.first_child ? seq[i].ntok : t0 + t.toks);
+      t.ctx = seq[i].base + 1 + (P.first_child ? 0 : t0);
+      t.kind = t.kbeg > 0 ? 2 : 0;
+    }
+    t.two = t.toks > tt;
+    t.blocks = (t.kend - t.kbeg + kKeyBlock - 1) / kKeyBlock;
+    return t;
+  };
+  int tiles = 0, cost = 0;
+  for (int own = P.group ? 0 : 1; own < 2; ++own)
     for (int i0 = 0; i0 < n; i0 += 1024) {
       const int i = i0 + tid;
-      int cnt = 0;
+      int cnt = 0, sum = 0;
       if (i < n) {
-        if (pass == 0) {
-          if (seq[i].leader == i && seq[i].shared > 0) cnt = (seq[i].gsize * P.N + 2 * tt - 1) / (2 * tt);
-        } else {
-          cnt = (seq[i].ntok + 2 * tt - 1) / (2 * tt);
+        if (own) cnt = (seq[i].ntok + 2 * tt - 1) / (2 * tt);
+        else if (seq[i].leader == i && seq[i].shared > 0) cnt = (seq[i].gsize * P.N + 2 * tt - 1) / (2 * tt);
+        for (int k = 0; k < cnt; ++k) {
+          const KvTile t = tile_of(i, k, own);
+          sum += (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads;
         }
       }
-      int sum;
-      const int at = tiles + block_scan(cnt, part, &sum);
-      if (i < n) (pass ? P.plan.suf0 : P.plan.pre0)[i] = at;
+      int all, all_cost;
+      const int at = tiles + block_scan(cnt, part, &all);
+      int before = cost + block_scan(sum, part, &all_cost);
+      if (i < n) (own ? P.plan.suf0 : P.plan.pre0)[i] = at;
       for (int k = 0; k < cnt; ++k) {
-        KvTile t = {};
-        const int t0 = 2 * tt * k;
-        t.tok0 = i * P.N + t0;
-        t.seq_row = seq[i].row;
-        if (pass == 0) {
-          t.toks = min(2 * tt, seq[i].gsize * P.N - t0);
-          t.kend = t.ctx = seq[i].shared;
-          t.kind = 1;
-        } else {
-          t.toks = min(2 * tt, seq[i].ntok - t0);
-          t.kbeg = seq[i].shared;
-          // a chain's tile sees no further than its last token, and all of it
-          // up to its first; a tree's nodes all see the root
-          t.kend = seq[i].base + (P.first_child ? seq[i].ntok : t0 + t.toks);
-          t.ctx = seq[i].base + 1 + (P.first_child ? 0 : t0);
-          t.kind = t.kbeg > 0 ? 2 : 0;
-        }
-        t.two = t.toks > tt;
-        t.blocks = (t.kend - t.kbeg + kKeyBlock - 1) / kKeyBlock;
-        t.cost0 = 0;
+        KvTile t = tile_of(i, k, own);
+        t.cost0 = before;
+        before += (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads;
         P.plan.tile[at + k] = t;
+        if (at + k < kTilesHere) costs[at + k] = t.cost0;
       }
-      tiles += sum;
+      tiles += all;
+      cost += all_cost;
     }
-  __syncthreads();
-  int cost = 0;
-  for (int t0 = 0; t0 < tiles; t0 += 1024) {
-    const int t = t0 + tid;
-    int sum;
-    const int at = block_scan(t < tiles ? (P.plan.tile[t].blocks * block_cost(P.plan.tile[t]) +
-                                           unit_cost(P.plan.tile[t])) * c.kv_heads : 0,
-                              part, &sum);
-    if (t < tiles) P.plan.tile[t].cost0 = cost + at;
-    cost += sum;
-  }
   __syncthreads();
   // at least a block's cost lies between two shares, so no two begin in one block
   const int ctas = cost ? min(kKvCtas, max(1, cost / kBlockCost2)) : 0;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
     int lo = 0, hi = tiles - 1;  // the last tile that begins at or before b
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (P.plan.tile[mid].cost0 <= b) lo = mid;
+      if ((mid < kTilesHere ? costs[mid] : P.plan.tile[mid].cost0) <= b) lo = mid;
       else hi = mid - 1;
     }
     // the share begins in unit (lo, y) at block z: the first of which no cost
@@ -1222,9 +1223,8 @@ __global__ void __launch_bounds__(256) join_cut_kernel(AttendParams P) {
   }
   const int b = blockIdx.x / kJoinParts + 1, part = blockIdx.x % kJoinParts;
   const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
-  if (b >= ctas) return;
   const int4 st = P.plan.start[b], before = P.plan.start[b - 1];
-  if (st.z == 0 || (before.x == st.x && before.y == st.y && before.z > 0)) return;
+  if (b >= ctas || st.z == 0 || (before.x == st.x && before.y == st.y && before.z > 0)) return;
   const KvTile t = P.plan.tile[st.x];
   const int2 c = unit_ctas(t, st.y, ctas, cost);
   const int tt = tile_tokens(P.rep), rows = t.toks * P.rep;
