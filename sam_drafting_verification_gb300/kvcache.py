@@ -88,14 +88,22 @@ class KVPlan:
     sequence (0: takes part), and the device memory that kv_append and
     kv_attend read and work in."""
 
-    def __init__(self, n, N, q_heads, grouped, buf):
-        self.n, self.N, self.q_heads, self.grouped, self.buf = n, N, q_heads, grouped, buf
-        self.bytes = buf.numel()
+    def __init__(self, n, N, q_heads, grouped, buf, nbytes, spare=None):
+        self.n, self.N, self.q_heads, self.grouped, self.buf, self.bytes = n, N, q_heads, grouped, buf, nbytes
         self.ptr = buf.data_ptr()
+        self._spare = spare
 
     @property
     def status(self):
+        self._spare = None   # the view may outlive the plan
         return self.buf[:4 * self.n].view(torch.int32)
+
+    def __del__(self):
+        # the cache's next plan on the stream may take the memory (allocating
+        # and freeing it anew takes as long as the rest of a small call)
+        spare = getattr(self, "_spare", None)
+        if spare is not None and len(spare) < 2:
+            spare.append(self.buf)
 
 
 class KVCache:
@@ -156,6 +164,7 @@ class KVCache:
                                                                          seqs, max_pages)))
         self._ref = ctypes.byref(self._desc)
         self._bytes = {}   # workspace sizes by call sizes
+        self._spare = {}   # by stream: memory of plans that are gone
 
     # -- helpers ---------------------------------------------------------------
     def _call(self, name, *args):
@@ -289,12 +298,28 @@ class KVCache:
                 need = self._bytes[key] = int(self.lib.kv_plan_bytes(self._ref, n, N, q_heads, gp is not None))
             if need == 0:
                 raise _b.SamspecError(f"sizes outside the limits: n={n}, N={N}, q_heads={q_heads}")
-            out = KVPlan(n, N, q_heads, gp is not None, torch.empty(need, dtype=torch.uint8, device=self.device))
+            out = self._new_plan(n, N, q_heads, gp is not None, need)
         elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.buf.device != self.device or \
                 (gp is not None and not out.grouped):
             raise ValueError("out: a plan of other sizes")
         self._call("kv_plan", rp, n, N, q_heads, np, fp, sp, gp, out.ptr, out.bytes)
         return out
+
+    def _new_plan(self, n, N, q_heads, grouped, need):
+        # memory of a plan that is gone, if one of about this size was used on
+        # this stream; not inside a graph capture, whose graph keeps its own
+        spare = buf = None
+        if self.device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            spare = self._spare.setdefault(_pkg._raw_stream(self.device.index), [])
+            for i, x in enumerate(spare):
+                if need <= x.numel() <= 4 * need:
+                    buf = spare.pop(i)
+                    break
+            else:
+                spare.clear()
+        if buf is None:
+            buf = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return KVPlan(n, N, q_heads, grouped, buf, need, spare)
 
     def _tokens(self, t, name, plan, heads):
         """t [n, N, heads, head_dim] of the cache's dtype, checked; its token

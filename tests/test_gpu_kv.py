@@ -381,6 +381,42 @@ def test_a_captured_step_follows_the_cache(ss, cuda_device):
             assert torch.equal(getattr(c, x), getattr(e, x)), (r, x)
 
 
+def test_plans_that_are_held_keep_their_memory(ss, cuda_device):
+    """A plan's memory is used again only once nothing of it can be read."""
+    lens = [100, 300, 17]
+    c, table = make(ss, cuda_device, lens, [4] * 3, 64, 2, 64)
+    q = queries(3, 4, 8, 64, BF16, cuda_device)
+    one, two = c.plan(4, 8), c.plan(4, 8, n_tok=i32([1, 2, 3], cuda_device))
+    assert one.ptr != two.ptr
+    check_attend(c, table, q, c.attend(0, one, q), lens, [4] * 3)
+    check_attend(c, table, q, c.attend(0, two, q), lens, [1, 2, 3])
+    ptr, status = one.ptr, one.status
+    del one
+    three = c.plan(4, 8, n_tok=i32([9, 9, 9], cuda_device))
+    assert three.ptr != ptr and status.tolist() == [0, 0, 0]
+    ptr = two.ptr
+    del two
+    four = c.plan(4, 8)
+    assert four.ptr == ptr
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        assert c.plan(4, 8).ptr != ptr
+    g = torch.cuda.CUDAGraph()
+    ptr = four.ptr
+    del four
+    with torch.cuda.graph(g):
+        plan = c.plan(4, 8)
+        out = c.attend(0, plan, q)
+        held = plan.ptr
+        del plan
+    assert held != ptr
+    for _ in range(3):
+        assert c.plan(4, 8).ptr != held
+    g.replay()
+    check_attend(c, table, q, out, lens, [4] * 3)
+
+
 def test_a_bad_sequence_gets_zeros_and_its_status(ss, cuda_device):
     lens, N = [100, 100, 100, 100, 100, 100], 4
     c, table = make(ss, cuda_device, lens, [4] * 6, 64, 2, 64, seed=8)
