@@ -150,7 +150,7 @@ int kv_append(const kv_cache* cache, int32_t layer, const void* d_plan, int32_t 
               int32_t rot, int32_t layout, float mscale, samspec_stream_t stream);
 
 /* Attention of the pass on one layer: d_out [n, N, q_heads, head_dim]
- * (contiguous, the cache's dtype) = softmax(scale * q k^T) v over the keys that
+ * (contiguous, 32-byte aligned, the cache's dtype) = softmax(scale * q k^T) v over the keys that
  * each token sees (query head h reads key head h / (q_heads / kv_heads)),
  * scale positive and finite.
  * Scores, softmax and sums in fp32; the probabilities are rounded to the

@@ -1420,7 +1420,7 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
   PlanLayout l;
   if (!plan_of(P.c, n, N, q_heads, plan_bytes, &l)) return SAMSPEC_ESIZE;
   if (q_stride < (int64_t)q_heads * P.c.head_dim) return SAMSPEC_EINVAL;
-  if ((reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_out)) % 16 != 0 || q_stride % 8 != 0 ||
+  if (reinterpret_cast<uintptr_t>(d_q) % 16 != 0 || reinterpret_cast<uintptr_t>(d_out) % 32 != 0 || q_stride % 8 != 0 ||
       reinterpret_cast<uintptr_t>(d_plan) % 256 != 0)
     return SAMSPEC_EALIGN;
   P.plan = plan_view(d_plan, l);

@@ -86,7 +86,8 @@ class Rope:
 class KVPlan:
     """The plan of one pass (KVCache.plan): `status` int32 [n], one word per
     sequence (0: takes part), and the device memory that kv_append and
-    kv_attend read and work in."""
+    kv_attend read and work in.  It belongs to the stream that it was made on:
+    where another one reads it, keep the plan until that one is done."""
 
     def __init__(self, n, N, q_heads, grouped, buf, nbytes, spare=None):
         self.n, self.N, self.q_heads, self.grouped, self.buf, self.bytes = n, N, q_heads, grouped, buf, nbytes

@@ -127,7 +127,7 @@ def test_append_and_attend_refuse_bad_arguments():
     for s in (0.0, -0.1, math.nan, math.inf):
         assert attend(scale=s) == bd.EINVAL
     assert attend(bytes=size - 1) == bd.ESIZE and attend(qs=1016) == bd.EINVAL and attend(qs=1028) == bd.EALIGN
-    assert attend(q=P + 8) == bd.EALIGN and attend(out=P + 2) == bd.EALIGN and attend(plan=P + 128) == bd.EALIGN
+    assert attend(q=P + 8) == bd.EALIGN and attend(out=P + 16) == bd.EALIGN and attend(plan=P + 128) == bd.EALIGN
 
 
 # ------------------------------------------------------------- the binding ----
