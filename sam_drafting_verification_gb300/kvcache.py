@@ -312,13 +312,18 @@ class KVCache:
         spare = buf = None
         if self.device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
             spare = self._spare.setdefault(_pkg._raw_stream(self.device.index), [])
-            for i, x in enumerate(spare):
-                if need <= x.numel() <= 4 * need:
-                    buf = spare.pop(i)
-                    break
-            else:
-                spare.clear()
+            try:
+                for _ in range(2):   # taken out before it is looked at: another thread may do the same
+                    x = spare.pop(0)
+                    if need <= x.numel() <= 4 * need:
+                        buf = x
+                        break
+                    spare.append(x)
+            except IndexError:
+                pass
         if buf is None:
+            if spare:
+                spare.clear()
             buf = torch.empty(need, dtype=torch.uint8, device=self.device)
         return KVPlan(n, N, q_heads, grouped, buf, need, spare)
 

@@ -251,3 +251,34 @@ def test_frequencies():
     for bad in (dict(rot=3), dict(rot=0), dict(rot=8, scaling="other"), dict(rot=8, base=-1.0), dict(rot=8, factor=0.0)):
         with pytest.raises(ValueError):
             ss.rope_frequencies(**bad)
+
+
+def test_plan_memory_is_taken_by_one_thread_alone(cache, monkeypatch):
+    """Another thread takes a plan's spare memory while this one looks at it:
+    each gets memory of its own, large enough."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(ss, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch, "empty", lambda n, **kw: Memory(n))
+    monkeypatch.setattr(cache, "device", torch.device("cuda", 0))
+    taken = []
+
+    class Memory:
+        def __init__(self, size, meanwhile=None):
+            self.size, self.meanwhile = size, meanwhile
+
+        def numel(self):
+            if self.meanwhile:
+                self.meanwhile()
+                self.meanwhile = None
+            return self.size
+
+        def data_ptr(self):
+            return P
+
+    def other_thread():
+        if spare:
+            taken.append(spare.pop(0))
+
+    spare = cache._spare[0] = [Memory(4096, other_thread), Memory(1024, other_thread)]
+    plan = cache._new_plan(2, 3, 4, False, 4096)
+    assert plan.buf.size >= 4096 and all(plan.buf is not t for t in taken)
