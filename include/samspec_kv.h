@@ -119,7 +119,8 @@ int kv_truncate(const kv_cache* cache, const int32_t* d_rows, int32_t n,
  * aligned, any content; it starts with the n status words, and holds the
  * workspace of kv_attend: one kv_attend at a time may use a plan (grouped:
  * non-zero where d_group is given, which takes more of it).  kv_attend is
- * given the same plan_bytes, n, N and q_heads as kv_plan.  A plan holds until
+ * given the same plan_bytes, n, N and q_heads as kv_plan, and it and kv_append
+ * a cache of the same sizes (but for layers and n_pages) and table.  A plan holds until
  * the cache's lengths or tables change.  Limits: n <= 2^20, N <= 2^16, q_heads
  * a multiple of kv_heads, at most 64 times as many, n * N * q_heads < 2^30
  * (with groups 2^29), and units of work times key blocks below 2^31 (a call

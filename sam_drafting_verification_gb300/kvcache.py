@@ -86,10 +86,12 @@ class Rope:
 class KVPlan:
     """The plan of one pass (KVCache.plan): `status` int32 [n], one word per
     sequence (0: takes part), and the device memory that kv_append and
-    kv_attend read and work in.  It belongs to the stream that it was made on:
+    kv_attend read and work in (of the cache that made it, or one of the same
+    sizes and table).  It belongs to the stream that it was made on:
     where another one reads it, keep the plan until that one is done."""
 
-    def __init__(self, n, N, q_heads, grouped, buf, nbytes, spare=None):
+    def __init__(self, n, N, q_heads, grouped, buf, nbytes, sizes, spare=None):
+        self.sizes = sizes   # of the cache: what it holds are that one's rows and pages
         self.n, self.N, self.q_heads, self.grouped, self.buf, self.bytes = n, N, q_heads, grouped, buf, nbytes
         self.ptr = buf.data_ptr()
         self._spare = spare
@@ -164,6 +166,7 @@ class KVCache:
                                     _DTYPES[k.dtype], *(int(x) for x in (layers, pages, page, kv_heads, head_dim,
                                                                          seqs, max_pages)))
         self._ref = ctypes.byref(self._desc)
+        self._sizes = (dev, self.page, self.kv_heads, self.head_dim, self.seqs, self.max_pages)
         self._bytes = {}   # workspace sizes by call sizes
         self._spare = {}   # by stream: memory of plans that are gone
 
@@ -300,7 +303,7 @@ class KVCache:
             if need == 0:
                 raise _b.SamspecError(f"sizes outside the limits: n={n}, N={N}, q_heads={q_heads}")
             out = self._new_plan(n, N, q_heads, gp is not None, need)
-        elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.buf.device != self.device or \
+        elif (out.n, out.N, out.q_heads) != (n, N, q_heads) or out.sizes != self._sizes or \
                 (gp is not None and not out.grouped):
             raise ValueError("out: a plan of other sizes")
         self._call("kv_plan", rp, n, N, q_heads, np, fp, sp, gp, out.ptr, out.bytes)
@@ -325,11 +328,13 @@ class KVCache:
             if spare:
                 spare.clear()
             buf = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return KVPlan(n, N, q_heads, grouped, buf, need, spare)
+        return KVPlan(n, N, q_heads, grouped, buf, need, self._sizes, spare)
 
     def _tokens(self, t, name, plan, heads):
         """t [n, N, heads, head_dim] of the cache's dtype, checked; its token
         stride in elements.  A view into a wider projection output will do."""
+        if plan.sizes is not self._sizes and plan.sizes != self._sizes:
+            raise ValueError("the plan is one of a cache of other sizes")
         shape = (plan.n, plan.N, heads, self.head_dim)
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a CUDA tensor")

@@ -282,3 +282,20 @@ def test_plan_memory_is_taken_by_one_thread_alone(cache, monkeypatch):
     spare = cache._spare[0] = [Memory(4096, other_thread), Memory(1024, other_thread)]
     plan = cache._new_plan(2, 3, 4, False, 4096)
     assert plan.buf.size >= 4096 and all(plan.buf is not t for t in taken)
+
+
+def test_a_plan_of_another_cache_is_refused(cache):
+    """A plan names rows and pages of its own cache, which another may not have."""
+    k = torch.zeros((2, 5, 2, 16, 64), dtype=torch.bfloat16)
+    other = ss.KVCache.wrap(k, k.clone(), i32(3, 2), i32(3), i32(3), i32(5), i32(1))
+    same = ss.KVCache.wrap(k, k.clone(), *(getattr(cache, f) for f in ("table", "lens", "held", "refs", "free")))
+    plan = cache.plan(3, 4, rows=i32(2), n_tok=i32(2))
+    q, kv = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 3, 2, 64), dtype=torch.bfloat16)
+    cache.rec.calls.clear()
+    for call in (lambda c: c.attend(0, plan, q), lambda c: c.append(0, plan, q, kv, kv),
+                 lambda c: c.append(0, plan, None, kv, kv), lambda c: c.plan(3, 4, rows=i32(2), out=plan)):
+        with pytest.raises(ValueError):
+            call(other)
+    assert names(cache) == []
+    same.attend(0, plan, q)
+    same.append(0, plan, q, kv, kv)
