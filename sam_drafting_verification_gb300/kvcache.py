@@ -224,7 +224,7 @@ class KVCache:
             most, np = min(self.max_pages * self.page, 1 << 30), self._i32(n_tok, "n_tok", (n,))
         else:
             n, rp = self._rows(rows)
-            most, np = int(n_tok), None
+            most, np = max(-1, min(int(n_tok), (1 << 31) - 1)), None   # (the call takes 32 bits)
         st = self._status(n, out)
         need = self._bytes.get(n)
         if need is None:

@@ -299,3 +299,10 @@ def test_a_plan_of_another_cache_is_refused(cache):
     assert names(cache) == []
     same.attend(0, plan, q)
     same.append(0, plan, q, kv, kv)
+
+
+def test_reserve_takes_a_number_past_32_bits_as_too_many(cache):
+    for ask, got in ((1 << 32, (1 << 31) - 1), ((1 << 32) + 4, (1 << 31) - 1), (-(1 << 32), -1), (7, 7)):
+        cache.rec.calls.clear()
+        cache.reserve(None, ask)
+        assert [a[3] for n, a in cache.rec.calls if n == "kv_reserve"] == [got]
