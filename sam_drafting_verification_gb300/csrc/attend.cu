@@ -171,10 +171,19 @@ constexpr int kBlockCost2 = 2;
 __device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? kBlockCost2 : 1; }
 __device__ __forceinline__ int unit_cost(const KvTile& t) { return t.two || t.kind ? 4 : 2; }
 
-__global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
+// The CTAs [c0, c1] that hold the blocks of unit (tile t, head h): those of its
+// first and its last block, each the last that begins at or before it.
+__device__ __forceinline__ int2 unit_ctas(const KvTile& t, int h, int ctas, int cost) {
+  const int bc = block_cost(t), uc = unit_cost(t);
+  const int64_t b0 = t.cost0 + h * (t.blocks * bc + uc) + uc + 1;
+  return {(int)((b0 * ctas - 1) / cost), (int)(((b0 + (t.blocks - 1) * bc) * ctas - 1) / cost)};
+}
+
+__global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P) {
   constexpr int kTilesHere = 8192;
   __shared__ int part[32];
   __shared__ int costs[kTilesHere];
+  __shared__ int4 starts[kKvCtas];
   const KvView& c = P.c;
   const int tid = threadIdx.x, n = P.n;
   wait_for_previous();
@@ -257,8 +266,10 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
   __syncthreads();
   // at least a block's cost lies between two shares, so no two begin in one block
   const int ctas = cost ? min(kKvCtas, max(1, cost / kBlockCost2)) : 0;
-  for (int x = tid; x <= ctas; x += 1024) {
-    const int b = ctas ? (int)((int64_t)x * cost / ctas) : 0;
+  int4 start = {tiles, 0, 0, 0};
+  KvTile at;
+  if (tid < ctas) {
+    const int b = (int)((int64_t)tid * cost / ctas);
     int lo = 0, hi = tiles - 1;  // the last tile that begins at or before b
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -267,22 +278,34 @@ __global__ void __launch_bounds__(1024) plan_units_kernel(PlanParams P) {
     }
     // the share begins in unit (lo, y) at block z: the first of which no cost
     // lies before b
-    int4 s = {tiles, 0, 0, 0};
-    if (x < ctas) {
-      const KvTile t = P.plan.tile[lo];
-      const int bc = block_cost(t), uc = unit_cost(t), u = t.blocks * bc + uc;
-      s.x = lo;
-      s.y = (b - t.cost0) / u;
-      s.z = max(((b - t.cost0) % u - uc + bc - 1) / bc, 0);
-      if (s.z == t.blocks) {  // behind the unit's last block
-        s.z = 0;
-        if (++s.y == c.kv_heads) {
-          s.y = 0;
-          ++s.x;
-        }
+    at = P.plan.tile[lo];
+    const int bc = block_cost(at), uc = unit_cost(at), u = at.blocks * bc + uc;
+    start.x = lo;
+    start.y = (b - at.cost0) / u;
+    start.z = max(((b - at.cost0) % u - uc + bc - 1) / bc, 0);
+    if (start.z == at.blocks) {  // behind the unit's last block
+      start.z = 0;
+      if (++start.y == c.kv_heads) {
+        start.y = 0;
+        ++start.x;
       }
     }
-    P.plan.start[x] = s;
+    starts[tid] = start;
+  }
+  if (tid <= ctas) P.plan.start[tid] = start;
+  __syncthreads();
+  if (tid < kKvCtas) {
+    KvJoin j = {};
+    if (tid < ctas && start.z > 0) {
+      // inside a unit: CTA tid - 1 holds what is before, all of it unless its
+      // share begins inside the same one
+      const int4 before = starts[tid - 1];
+      const bool same = before.x == start.x && before.y == start.y;
+      if (!same || before.z == 0)
+        j = {at.tok0, at.toks, start.y, unit_ctas(at, start.y, ctas, cost).y - tid + 2,
+             (2 * (tid - 1) + !same) * P.plan.slot_rows, 2 * tid * P.plan.slot_rows, {0, 0}};
+    }
+    P.plan.join[tid] = j;
   }
   // CTAs without a share begin where the last one ends
   for (int x = ctas + 1 + tid; x <= kKvCtas; x += 1024) P.plan.start[x] = {tiles, 0, 0, 0};
@@ -1142,13 +1165,6 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ---- joining partial results ---------------------------------------------------
-// The CTAs [c0, c1] that hold the blocks of unit (tile t, head h): those of its
-// first and its last block, each the last that begins at or before it.
-__device__ __forceinline__ int2 unit_ctas(const KvTile& t, int h, int ctas, int cost) {
-  const int bc = block_cost(t), uc = unit_cost(t);
-  const int64_t b0 = t.cost0 + h * (t.blocks * bc + uc) + uc + 1;
-  return {(int)((b0 * ctas - 1) / cost), (int)(((b0 + (t.blocks - 1) * bc) * ctas - 1) / cost)};
-}
 // Row `at` of a cut unit: where its part of CTA c0 lies (that one's first
 // segment, or its last), and of CTA c0 + 1 (the first; the others follow 2 *
 // slot_rows apart).
@@ -1156,6 +1172,84 @@ __device__ __forceinline__ int2 part_slots(const PlanView& p, int ti, int h, int
   const int4 st = p.start[c0];
   const bool begins = st.x == ti && st.y == h && st.z == 0;
   return {(2 * c0 + !begins) * p.slot_rows + at, 2 * (c0 + 1) * p.slot_rows + at};
+}
+
+// 16 columns of a row (from d0 on) of its parts, added up by a thread, two in
+// flight at once: `cnt` of them, the first at slot `first`, the others from
+// `rest` on.
+template <typename T, int D>
+__device__ __forceinline__ void join_piece(const AttendParams& P, int64_t row, int d0, int cnt, int first, int rest) {
+  using H = Type16<T>;
+  constexpr int kDeep = 2;
+  float m = -INFINITY, l = 0.f, o[16] = {};
+#pragma unroll 1
+  for (int q = 0; q < cnt; q += kDeep) {
+    float2 z[kDeep];
+    float4 a[kDeep][4];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int k = q + e;
+      if (k < cnt) {
+        const int64_t slot = k == 0 ? first : rest + (int64_t)(k - 1) * 2 * P.plan.slot_rows;
+        z[e] = P.plan.ml[slot];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) a[e][d] = reinterpret_cast<const float4*>(P.plan.o + slot * D + d0)[d];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e)
+      if (q + e < cnt) {
+        const float mn = fmaxf(m, z[e].x), mm = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - mm), g = exp2f(z[e].x - mm);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          o[4 * d] = o[4 * d] * f + a[e][d].x * g;
+          o[4 * d + 1] = o[4 * d + 1] * f + a[e][d].y * g;
+          o[4 * d + 2] = o[4 * d + 2] * f + a[e][d].z * g;
+          o[4 * d + 3] = o[4 * d + 3] * f + a[e][d].w * g;
+        }
+        l = l * f + z[e].y * g;
+        m = mn;
+      }
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint32_t h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+  store32(P.out + (row * D + d0) * 2, h);
+}
+
+// Without groups only units that were cut among CTAs are joined: `parts` CTAs
+// for each, a thread 16 columns of a row.  Bound by latency (the plan holds
+// where a unit's parts lie, since finding that here took 3 reads after one
+// another) and, for units of 256 rows, by the parts' bytes: of prompt chunks'
+// 114 us the join takes 13.  (Parts added up by the CTA that is done last, in
+// the attention kernel: 27 us, on one SM what this spreads over eight.)
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_cut_kernel(AttendParams P, int parts) {
+  wait_for_previous();
+  let_next_start();
+  const int joins = (kKvCtas - 1) * parts;
+  if (blockIdx.x >= joins) {
+    // four tokens a warp, neighbours to different ones: those that take no part
+    // lie side by side
+    const int warps = (gridDim.x - joins) * 8, lane = threadIdx.x & 31;
+    const int t0 = (blockIdx.x - joins) * 8 + (threadIdx.x >> 5), tok = t0 + lane * warps;
+    const bool dead = lane < 4 && tok < P.n * P.N && tok % P.N >= P.plan.seq[tok / P.N].ntok;
+    for (uint32_t todo = __ballot_sync(kFullMask, dead); todo; todo &= todo - 1) {
+      uint4* out = reinterpret_cast<uint4*>(P.out + (int64_t)(t0 + (__ffs(todo) - 1) * warps) * P.q_heads * D * 2);
+      for (int x = lane; x < P.q_heads * (D / 8); x += 32) out[x] = uint4{0, 0, 0, 0};
+    }
+    return;
+  }
+  const KvJoin j = P.plan.join[blockIdx.x / parts + 1];
+  const int tt = tile_tokens(P.rep);
+  for (int x = blockIdx.x % parts * 256 + threadIdx.x; x < j.toks * P.rep * (D / 16); x += 256 * parts) {
+    const int r = x / (D / 16), lt = P.rep_div(r);
+    const int at = r + (lt >= tt ? kRows - tt * P.rep : 0);  // the second tile's rows from kRows on
+    const int64_t row = ((int64_t)j.tok0 + lt) * P.q_heads + j.head * P.rep + r - lt * P.rep;
+    join_piece<T, D>(P, row, x % (D / 16) * 16, j.parts, j.first + at, j.rest + at);
+  }
 }
 
 // A row's parts added up by a warp, four in flight at once: `cnt` of them, the
@@ -1198,42 +1292,6 @@ __device__ __forceinline__ void join_row(const AttendParams& P, int64_t row, int
   uint32_t* out = reinterpret_cast<uint32_t*>(P.out + row * D * 2) + lane * (kPer / 2);
 #pragma unroll
   for (int e = 0; e < kPer / 2; ++e) out[e] = H::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
-}
-
-// Without groups only units that were cut among CTAs are joined: where a share
-// begins inside a unit, and no share before it does in the same one, the CTA
-// (boundary, 1 of kJoinParts) joins a part of that unit's rows.  The CTAs behind
-// these write the zeros of tokens that take no part.
-constexpr int kJoinParts = 8;
-template <typename T, int D>
-__global__ void __launch_bounds__(256) join_cut_kernel(AttendParams P) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_for_previous();
-  let_next_start();
-  if (blockIdx.x >= (kKvCtas - 1) * kJoinParts) {
-    // 4 tokens a warp (32 took 43 us where half of 4000 tokens take no part)
-    const int t0 = ((blockIdx.x - (kKvCtas - 1) * kJoinParts) * 8 + warp) * 4, tok = t0 + lane;
-    bool dead = false;
-    if (lane < 4 && tok < P.n * P.N) dead = tok % P.N >= P.plan.seq[tok / P.N].ntok;
-    for (uint32_t todo = __ballot_sync(kFullMask, dead); todo; todo &= todo - 1) {
-      uint4* out = reinterpret_cast<uint4*>(P.out + (int64_t)(t0 + __ffs(todo) - 1) * P.q_heads * D * 2);
-      for (int x = lane; x < P.q_heads * (D / 8); x += 32) out[x] = uint4{0, 0, 0, 0};
-    }
-    return;
-  }
-  const int b = blockIdx.x / kJoinParts + 1, part = blockIdx.x % kJoinParts;
-  const int ctas = P.plan.hdr[kHdrCtas], cost = P.plan.hdr[kHdrCost];
-  const int4 st = P.plan.start[b], before = P.plan.start[b - 1];
-  if (b >= ctas || st.z == 0 || (before.x == st.x && before.y == st.y && before.z > 0)) return;
-  const KvTile t = P.plan.tile[st.x];
-  const int2 c = unit_ctas(t, st.y, ctas, cost);
-  const int tt = tile_tokens(P.rep), rows = t.toks * P.rep;
-  for (int x = part * 8 + warp; x < rows; x += 8 * kJoinParts) {
-    const int lt = x / P.rep, j = x % P.rep;
-    const int2 s = part_slots(P.plan, st.x, st.y, c.x, lt / tt * kRows + lt % tt * P.rep + j);
-    const int64_t row = ((int64_t)t.tok0 + lt) * P.q_heads + st.y * P.rep + j;
-    join_row<T, D>(P, row, c.y - c.x + 1, 0, 0, 0, s.x, s.y, lane);
-  }
 }
 
 // With groups: a warp takes 8 rows, a lane finds where one row's parts lie
@@ -1350,11 +1408,12 @@ int attend(AttendParams P, const CUtensorMap& mk, const CUtensorMap& mv, const C
   if (launch_after(attend_kernel<T, D>, kKvCtas, 384, Ring<D>::kBytes, s, P, mk, mv, mq) != cudaSuccess)
     return SAMSPEC_ECUDA;
   const int64_t toks = (int64_t)P.n * P.N;
+  const int parts = (P.plan.slot_rows * (D / 16) + 255) / 256;
   const cudaError_t e =
       P.plan.store ? launch_after(join_rows_kernel<T, D>, (unsigned)((toks * P.q_heads + 8 * kJoinRows - 1) / (8 * kJoinRows)),
                                   256, 0, s, P)
-                   : launch_after(join_cut_kernel<T, D>, (unsigned)((kKvCtas - 1) * kJoinParts + (toks + 31) / 32), 256, 0,
-                                  s, P);
+                   : launch_after(join_cut_kernel<T, D>, (unsigned)((kKvCtas - 1) * parts + (toks + 31) / 32), 256, 0, s, P,
+                                  parts);
   return e == cudaSuccess ? launched() : SAMSPEC_ECUDA;
 }
 

@@ -132,11 +132,18 @@ struct KvTile {
   int32_t cost0;       // cost of all heads of the tiles before
   int32_t pad[2];
 };
+// a unit that was cut among CTAs: at the CTA behind its first part's
+struct KvJoin {
+  int32_t tok0, toks;  // its tokens (0: no unit is first cut here)
+  int32_t head, parts;
+  int32_t first, rest;  // where its first part's rows lie, and the second's; the others 2 * slot_rows apart
+  int32_t pad[2];
+};
 inline __host__ __device__ int tile_tokens(int rep) { return kRows / rep; }
 enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4, kHdrInts = 16 };
 
 struct PlanLayout {
-  size_t status, hdr, seq, node, suf0, pre0, tile, start, ml, o, bytes;
+  size_t status, hdr, seq, node, suf0, pre0, tile, start, join, ml, o, bytes;
   int32_t max_tiles;
   int32_t slot_rows;  // rows of a cut unit's part
   int64_t store;      // rows of each of the two stores of whole units (grouped plans)
@@ -173,6 +180,7 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
   p.pre0 = take(4 * (size_t)n);
   p.tile = take(sizeof(KvTile) * (size_t)p.max_tiles);
   p.start = take(16 * (kKvCtas + 1));
+  p.join = take(sizeof(KvJoin) * kKvCtas);
   p.ml = take(8 * (size_t)p.part_rows);
   p.o = take(4 * (size_t)p.part_rows * c.head_dim);
   p.bytes = at;
@@ -188,6 +196,7 @@ struct PlanView {
   int32_t* pre0;   // first tile of a group's shared keys (at the leader)
   KvTile* tile;
   int4* start;     // where each CTA's share begins: tile, head, block
+  KvJoin* join;    // the cut units (plans without groups)
   float2* ml;      // partial results: running maximum (base 2) and sum ...
   float* o;        // ... and the sums of p v
   int32_t slot_rows;
@@ -199,8 +208,9 @@ inline PlanView plan_view(void* d_plan, const PlanLayout& p) {
           reinterpret_cast<KvSeq*>(b + p.seq),      reinterpret_cast<int2*>(b + p.node),
           reinterpret_cast<int32_t*>(b + p.suf0),   reinterpret_cast<int32_t*>(b + p.pre0),
           reinterpret_cast<KvTile*>(b + p.tile),    reinterpret_cast<int4*>(b + p.start),
-          reinterpret_cast<float2*>(b + p.ml),      reinterpret_cast<float*>(b + p.o),
-          p.slot_rows,                              p.store};
+          reinterpret_cast<KvJoin*>(b + p.join),    reinterpret_cast<float2*>(b + p.ml),
+          reinterpret_cast<float*>(b + p.o),        p.slot_rows,
+          p.store};
 }
 
 }  // namespace samspec
