@@ -27,15 +27,10 @@ struct PlanParams {
   int n, N, q_heads, rep;
 };
 
-// One warp a sequence: its lengths and pages checked, the tree's depths and
+// A warp: its sequence's lengths and pages checked, the tree's depths and
 // ancestors, the pages that it shares with the first sequence of its group.
-__global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
+__device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int lane) {
   const KvView& c = P.c;
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  wait_for_previous();
-  let_next_start();
-  if (i >= P.n) return;
   int st = SAMSPEC_ST_OK;
   const int row = P.rows ? P.rows[i] : i;
   const int nt = P.first_child ? P.N : P.n_tok ? P.n_tok[i] : P.N;
@@ -157,6 +152,12 @@ __global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
     P.plan.seq[i] = {row, base, st ? 0 : nt, leader, lcp, 0, 0, 0};
   }
 }
+__global__ void __launch_bounds__(256) plan_sequences_kernel(PlanParams P) {
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  wait_for_previous();
+  let_next_start();
+  if (i < P.n) plan_sequence(P, i, threadIdx.x & 31);
+}
 
 // One CTA: what a group reads once, the units of work and their order, and
 // each persistent CTA's equal share of the key blocks.
@@ -179,7 +180,7 @@ __device__ __forceinline__ int2 unit_ctas(const KvTile& t, int h, int ctas, int 
   return {(int)((b0 * ctas - 1) / cost), (int)(((b0 + (t.blocks - 1) * bc) * ctas - 1) / cost)};
 }
 
-__global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P) {
+__global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P, bool sequences) {
   constexpr int kTilesHere = 8192;
   __shared__ int part[32];
   __shared__ int costs[kTilesHere];
@@ -188,6 +189,10 @@ __global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P) {
   const int tid = threadIdx.x, n = P.n;
   wait_for_previous();
   let_next_start();
+  if (sequences) {
+    if (tid >> 5 < n) plan_sequence(P, tid >> 5, tid & 31);
+    __syncthreads();
+  }
   const int tt = tile_tokens(P.rep);
   KvSeq* seq = P.plan.seq;
   if (P.group) {
@@ -1461,8 +1466,11 @@ int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, 
   P.q_heads = q_heads;
   P.rep = q_heads / P.c.kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_after(plan_sequences_kernel, (n + 7) / 8, 256, 0, s, P) != cudaSuccess ||
-      launch_after(plan_units_kernel, 1, 1024, 0, s, P) != cudaSuccess)
+  // up to 32 sequences, a warp each, are judged by the units' CTA: one launch
+  // less (at 64, two a warp, a step of 64 trees took 232 us instead of 224)
+  const bool few = n <= 32;
+  if ((!few && launch_after(plan_sequences_kernel, (n + 7) / 8, 256, 0, s, P) != cudaSuccess) ||
+      launch_after(plan_units_kernel, 1, 1024, 0, s, P, few) != cudaSuccess)
     return SAMSPEC_ECUDA;
   return launched();
 }
