@@ -32,6 +32,11 @@ struct PlanParams {
 __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int lane) {
   const KvView& c = P.c;
   int st = SAMSPEC_ST_OK;
+  int first = -1, next = -1;  // (read before the lengths are known)
+  if (P.first_child && lane < P.N) {
+    first = P.first_child[(int64_t)i * P.N + lane];
+    next = P.next_sibling[(int64_t)i * P.N + lane];
+  }
   const int row = P.rows ? P.rows[i] : i;
   const int nt = P.first_child ? P.N : P.n_tok ? P.n_tok[i] : P.N;
   bool twice = false;
@@ -53,14 +58,7 @@ __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int la
   if (P.first_child && st == SAMSPEC_ST_OK) {
     // lane p walks its children (links only point to larger numbers, so each
     // walk ends) and is every child's parent
-    const int32_t* fc = P.first_child + (int64_t)i * P.N;
-    const int32_t* ns = P.next_sibling + (int64_t)i * P.N;
     const int N = P.N;
-    int first = -1, next = -1;
-    if (lane < N) {
-      first = fc[lane];
-      next = ns[lane];
-    }
     bool bad = lane < N && ((first != -1 && (first <= lane || first >= N)) ||
                             (next != -1 && (next <= lane || next >= N)) || (lane == 0 && next != -1));
     if (__any_sync(kFullMask, bad)) {
@@ -104,12 +102,18 @@ __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int la
     const int pages = (int)(((int64_t)base + nt + c.page - 1) >> c.log_page);
     const int full = base >> c.log_page;
     bool bad = false, lent = false;
-    for (int k = lane; k < pages; k += 32) {
-      const int p = t[k];
-      const bool out = p < 0 || p >= c.n_pages;
-      bad |= out;
-      // a page that is written has to be the sequence's alone
-      if (!out && k >= full && nt > 0) lent |= c.refs[p] > 1;
+    for (int k0 = lane; k0 < pages; k0 += 128) {  // four reads of a lane in flight
+      int p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = k0 + 32 * e < pages ? t[k0 + 32 * e] : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = k0 + 32 * e;
+        const bool out = p[e] < 0 || p[e] >= c.n_pages;
+        bad |= out;
+        // a page that is written has to be the sequence's alone
+        if (!out && k >= full && k < pages && nt > 0) lent |= c.refs[p[e]] > 1;
+      }
     }
     if (__any_sync(kFullMask, bad)) st = SAMSPEC_ST_PAGE;
     else if (__any_sync(kFullMask, lent)) st = SAMSPEC_ST_CAPACITY;
@@ -134,11 +138,17 @@ __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int la
         const int m = min(full, lfull);
         const int32_t* tl = c.table + (int64_t)(m ? lrow : 0) * c.max_pages;
         int same = m;
-        for (int k = 0; k < m; k += 32) {
-          const uint32_t differ = __ballot_sync(kFullMask, k + lane < m && t[k + lane] != tl[k + lane]);
-          if (differ) {
-            same = k + __ffs(differ) - 1;
-            break;
+        for (int k0 = 0; k0 < m && same == m; k0 += 128) {
+          bool d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = k0 + 32 * e + lane;
+            d[e] = k < m && t[k] != tl[k];
+          }
+#pragma unroll
+          for (int e = 3; e >= 0; --e) {  // the first that differs stays
+            const uint32_t differ = __ballot_sync(kFullMask, d[e]);
+            if (differ) same = k0 + 32 * e + __ffs(differ) - 1;
           }
         }
         lcp = same << c.log_page;
