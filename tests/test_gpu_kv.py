@@ -673,3 +673,58 @@ def test_many_sequences_and_a_large_pool(ss, cuda_device):
     assert c.truncate(i32(half, dev)).tolist() == [0] * len(half)
     m.truncate(half, [0] * len(half))
     same_state(c, m)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 70])
+@pytest.mark.parametrize("tree", [False, True])
+def test_plans_of_few_and_of_many_sequences(ss, cuda_device, n, tree):
+    """Up to 32 sequences are planned in one launch, more in two: the same
+    statuses and results."""
+    dev, N, Q = cuda_device, 9, 6
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, 400, n)]
+    n_tok = [N] * n if tree else [int(x) for x in rng.integers(0, N + 1, n)]
+    c, table = make(ss, dev, lens, [N] * n, 32, 2, 64, seed=n)
+    parent = ref.random_parents(rng, n, N)
+    fc, ns = (i32(x, dev) for x in ref.links(parent))
+    want = [0] * n
+    last = n - 1
+    c.held[last] = 0 if lens[last] else -1          # fewer pages than tokens
+    c.table[1, lens[1] // 32] = c.pages             # a page outside the pool
+    want[last], want[1] = ref.ST_PAGE, ref.ST_PAGE
+    if tree:
+        fc[n // 2, 0] = N
+    else:
+        n_tok[n // 2] = N + 1
+    want[n // 2] = ref.ST_BADDRAFT
+    if not tree:
+        n_tok[1] = N
+    rows = list(range(n))
+    rows[3], want[3] = n, ref.ST_ROW
+    rows[5], want[5], want[6] = 6, ref.ST_ROW, ref.ST_ROW
+    q = queries(n, N, Q, 64, BF16, dev)
+    plan = c.plan(N, Q, rows=i32(rows, dev), n_tok=None if tree else i32(n_tok, dev), tree=(fc, ns) if tree else None)
+    out = c.attend(0, plan, q)
+    assert plan.status.tolist() == want
+    takes = [0 if st else t for st, t in zip(want, n_tok)]
+    check_attend(c, table, q, out, lens, takes, parent if tree else None)
+
+
+@pytest.mark.parametrize("at", [0, 5, 100, 127, 128, 133])
+def test_a_group_shares_pages_up_to_the_first_that_differs(ss, cuda_device, at):
+    dev, page, N, Q = cuda_device, 16, 2, 4
+    lens = [16 * 135 + x for x in (3, 40, 17, 100)]
+    n = len(lens)
+    c, table = make(ss, dev, lens, [N] * n, page, 1, 128, shared=([0] * n, 16 * 135), seed=at)
+    fresh = next(p for p in range(c.pages) if p not in set(table.flatten().tolist()))
+    old = int(table[2, at])
+    c.k[:, fresh], c.v[:, fresh] = c.k[:, old].neg(), c.v[:, old].neg()   # other keys there, so that a wrong page shows
+    table[2, at] = fresh
+    c.table[2, at] = fresh
+    c.refs[fresh] = 1
+    c.refs[old] -= 1
+    q = queries(n, N, Q, 128, BF16, dev)
+    plan = c.plan(N, Q, group=i32([7] * n, dev))
+    out = c.attend(0, plan, q)
+    assert (plan.status == 0).all()
+    check_attend(c, table, q, out, lens, [N] * n)
