@@ -166,6 +166,9 @@ class KVCache:
                                     _DTYPES[k.dtype], *(int(x) for x in (layers, pages, page, kv_heads, head_dim,
                                                                          seqs, max_pages)))
         self._ref = ctypes.byref(self._desc)
+        if self.lib.kv_reserve_workspace_bytes(self._ref, 1) == 0:   # what every call would refuse
+            raise _b.SamspecError(f"a cache outside the limits: {tuple(k.shape)}, {seqs} x {max_pages} pages, "
+                                  "or k and v not 16-byte aligned")
         self._sizes = (dev, self.page, self.kv_heads, self.head_dim, self.seqs, self.max_pages)
         self._bytes = {}   # workspace sizes by call sizes
         self._spare = {}   # by stream: memory of plans that are gone

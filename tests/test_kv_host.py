@@ -306,3 +306,15 @@ def test_reserve_takes_a_number_past_32_bits_as_too_many(cache):
         cache.rec.calls.clear()
         cache.reserve(None, ask)
         assert [a[3] for n, a in cache.rec.calls if n == "kv_reserve"] == [got]
+
+
+@pytest.mark.parametrize("page,D,max_pages,skew", [(48, 64, 3, 0), (8, 64, 3, 0), (16, 96, 3, 0), (16, 64, (1 << 20) + 1, 0),
+                                                   (16, 64, 3, 4)])
+def test_a_cache_outside_the_limits_is_refused_when_made(monkeypatch, page, D, max_pages, skew):
+    monkeypatch.setattr(ss, "_is_cuda", lambda t: True)
+    k = torch.zeros(skew + 2 * page * D, dtype=torch.bfloat16)[skew:].view(1, 2, 1, page, D)
+    tensors = (i32(1, max_pages), i32(1), i32(1), i32(2), i32(1))
+    with pytest.raises(bd.SamspecError):
+        ss.KVCache.wrap(k, k, *tensors)
+    good = torch.zeros((1, 2, 1, 16, 64), dtype=torch.bfloat16)
+    assert ss.KVCache.wrap(good, good, i32(1, 3), *tensors[1:]).page == 16
