@@ -177,10 +177,12 @@ constexpr int kMinShared = 128;  // tokens: less is read by each sequence for it
 // its streams; more where its results are partial, in fp32, or two tiles').
 // Measured: 256 trees over short histories 52 us with 4 for every unit and 46
 // with 2; groups of 16 with 880 own keys each 437 us with 2 and 418 with 4;
-// prompt chunks 148 us with 2 and 119 with 4.
+// prompt chunks (1000 tokens and up to 4000 before, 4 sequences) 114 us with 4
+// for a unit of two tiles, 110 with 5 and 106 with 6, 256-token chunks of 16
+// sequences 67.3, 66.9 and 71.
 constexpr int kBlockCost2 = 2;
 __device__ __forceinline__ int block_cost(const KvTile& t) { return t.two ? kBlockCost2 : 1; }
-__device__ __forceinline__ int unit_cost(const KvTile& t) { return t.two || t.kind ? 4 : 2; }
+__device__ __forceinline__ int unit_cost(const KvTile& t) { return t.two ? 5 : t.kind ? 4 : 2; }
 
 // The CTAs [c0, c1] that hold the blocks of unit (tile t, head h): those of its
 // first and its last block, each the last that begins at or before it.

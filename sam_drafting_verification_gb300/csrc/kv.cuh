@@ -163,7 +163,7 @@ inline PlanLayout plan_layout(const KvView& c, int32_t n, int32_t N, int32_t q_h
   const int64_t suf = (N + unit - 1) / unit * n;
   const int64_t pre = grouped ? ((int64_t)n * N + unit - 1) / unit + n : 0;
   // costs are counted in 32 bits
-  const int64_t blocks = ((int64_t)c.max_pages * c.page / kKeyBlock + 2) * 2 + 4;
+  const int64_t blocks = ((int64_t)c.max_pages * c.page / kKeyBlock + 2) * 2 + 5;
   if ((suf + pre) * blocks * c.kv_heads >= ((int64_t)1 << 31)) return p;
   p.max_tiles = (int32_t)(suf + pre);
   p.store = grouped ? (int64_t)n * N * q_heads : 0;
