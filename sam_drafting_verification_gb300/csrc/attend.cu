@@ -231,51 +231,70 @@ __global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P, bool 
   }
   // tiles of the groups' shared keys, then of each sequence's own; the costs
   // before each are kept in shared memory too, where the shares are looked up
-  auto tile_of = [&](int i, int k, bool own) {
+  auto tile_of = [&](const KvSeq& q, int i, int k, bool own) {
     KvTile t = {};
     const int t0 = 2 * tt * k;
     t.tok0 = i * P.N + t0;
-    t.seq_row = seq[i].row;
+    t.seq_row = q.row;
     if (!own) {
-      t.toks = min(2 * tt, seq[i].gsize * P.N - t0);
-      t.kend = t.ctx = seq[i].shared;
+      t.toks = min(2 * tt, q.gsize * P.N - t0);
+      t.kend = t.ctx = q.shared;
       t.kind = 1;
     } else {
-      t.toks = min(2 * tt, seq[i].ntok - t0);
-      t.kbeg = seq[i].shared;
+      t.toks = min(2 * tt, q.ntok - t0);
+      t.kbeg = q.shared;
       // a chain's tile sees no further than its last token, and all of it up
       // to its first; a tree's nodes all see the root
-      t.kend = seq[i].base + (P.first_child ? seq[i].ntok : t0 + t.toks);
-      t.ctx = seq[i].base + 1 + (P.first_child ? 0 : t0);
+      t.kend = q.base + (P.first_child ? q.ntok : t0 + t.toks);
+      t.ctx = q.base + 1 + (P.first_child ? 0 : t0);
       t.kind = t.kbeg > 0 ? 2 : 0;
     }
     t.two = t.toks > tt;
     t.blocks = (t.kend - t.kbeg + kKeyBlock - 1) / kKeyBlock;
     return t;
   };
+  // As many threads a sequence as it may have tiles, up to a warp: a prompt of
+  // 32768 tokens has 512 of them (the plan took 99 us with one thread, 16 with a
+  // warp); where a sequence has one, more threads cost 1 us.
+  int lanes = 32;
+  while (lanes > 1 && (n * lanes > 1024 || lanes * tt >= P.N)) lanes >>= 1;
+  const int sub = tid & (lanes - 1);
   int tiles = 0, cost = 0;
   for (int own = P.group ? 0 : 1; own < 2; ++own)
-    for (int i0 = 0; i0 < n; i0 += 1024) {
-      const int i = i0 + tid;
+    for (int i0 = 0; i0 < n; i0 += 1024 / lanes) {
+      const int i = i0 + tid / lanes;
       int cnt = 0, sum = 0;
+      KvSeq q = {};
       if (i < n) {
-        if (own) cnt = (seq[i].ntok + 2 * tt - 1) / (2 * tt);
-        else if (seq[i].leader == i && seq[i].shared > 0) cnt = (seq[i].gsize * P.N + 2 * tt - 1) / (2 * tt);
-        for (int k = 0; k < cnt; ++k) {
-          const KvTile t = tile_of(i, k, own);
-          sum += (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads;
-        }
+        q = seq[i];
+        if (own) cnt = (q.ntok + 2 * tt - 1) / (2 * tt);
+        else if (q.leader == i && q.shared > 0) cnt = (q.gsize * P.N + 2 * tt - 1) / (2 * tt);
       }
+      auto cost_of = [&](const KvTile& t) { return (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads; };
+      for (int k = sub; k < cnt; k += lanes) sum += cost_of(tile_of(q, i, k, own));
       int all, all_cost;
-      const int at = tiles + block_scan(cnt, part, &all);
+      int at = tiles + block_scan(sub == 0 ? cnt : 0, part, &all);
       int before = cost + block_scan(sum, part, &all_cost);
-      if (i < n) (own ? P.plan.suf0 : P.plan.pre0)[i] = at;
-      for (int k = 0; k < cnt; ++k) {
-        KvTile t = tile_of(i, k, own);
-        t.cost0 = before;
-        before += (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads;
-        P.plan.tile[at + k] = t;
-        if (at + k < kTilesHere) costs[at + k] = t.cost0;
+      at = __shfl_sync(kFullMask, at, 0, lanes);
+      before = __shfl_sync(kFullMask, before, 0, lanes);
+      if (i < n && sub == 0) (own ? P.plan.suf0 : P.plan.pre0)[i] = at;
+      const int most = __reduce_max_sync(kFullMask, cnt);
+      for (int k0 = 0; k0 < most; k0 += lanes) {
+        const int k = k0 + sub;
+        KvTile t = {};
+        if (k < cnt) t = tile_of(q, i, k, own);
+        const int mine = k < cnt ? cost_of(t) : 0;
+        int upto = mine;
+        for (int o = 1; o < lanes; o <<= 1) {
+          const int x = __shfl_up_sync(kFullMask, upto, o, lanes);
+          if (sub >= o) upto += x;
+        }
+        if (k < cnt) {
+          t.cost0 = before + upto - mine;
+          P.plan.tile[at + k] = t;
+          if (at + k < kTilesHere) costs[at + k] = t.cost0;
+        }
+        before += __shfl_sync(kFullMask, upto, lanes - 1, lanes);
       }
       tiles += all;
       cost += all_cost;
