@@ -728,3 +728,21 @@ def test_a_group_shares_pages_up_to_the_first_that_differs(ss, cuda_device, at):
     out = c.attend(0, plan, q)
     assert (plan.status == 0).all()
     check_attend(c, table, q, out, lens, [N] * n)
+
+
+@pytest.mark.parametrize("n,N,Q,H", [(8300, 1, 2, 1), (40, 600, 64, 1)])
+def test_more_tiles_than_shared_memory_holds(ss, cuda_device, n, N, Q, H):
+    """8300 short sequences of a tile each (beyond 8192 the shares are looked up
+    in memory), and sequences of many tiles, which several threads plan."""
+    dev = cuda_device
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, 40, n)]
+    n_tok = [int(x) for x in rng.integers(max(1, N - 300), N + 1, n)]
+    c, table = make(ss, dev, lens, n_tok, 16, H, 64, seed=n)
+    q = queries(n, N, Q, 64, BF16, dev)
+    plan = c.plan(N, Q, n_tok=i32(n_tok, dev))
+    out = c.attend(0, plan, q)
+    assert (plan.status == 0).all() and torch.isfinite(out).all()
+    some = [0, 1, n // 2, n - 2, n - 1] + [int(x) for x in rng.integers(0, n, 40 if N == 1 else 3)]
+    check_attend(c, table[some], q[some], out[some], [lens[b] for b in some], [n_tok[b] for b in some])
+    assert all((out[b, n_tok[b]:] == 0).all() for b in range(0, n, max(1, n // 40)))
