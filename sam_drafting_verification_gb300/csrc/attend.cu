@@ -946,8 +946,11 @@ __global__ void __launch_bounds__(384, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax ----
-    // A thread that gives up keeps taking part in every barrier and arrival
-    // of its segment, without work, so that no other waits for it.
+    // A thread that gives up keeps taking part in every bar.sync of its segment,
+    // without work, so that no other waits for it there.  It arrives on no
+    // mbarrier any more: that would hand on what it has not seen (a ring stage
+    // whose copy is still on its way would be asked for again, and its barrier's
+    // counts would run ahead); those who wait for it see the flag.
     const int w = warp >> 2;                 // stream
     const int row = (warp & 3) * 32 + lane;  // its lane of tensor memory
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -998,7 +1001,7 @@ __global__ void __launch_bounds__(384, 1)
         if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
-        if (row == 0) {
+        if (ok && row == 0) {
           // the product is done with the block's keys, the last one with the
           // queries (arrivals here, since each commit of the products' warp
           // takes the matrix unit 57 clocks)
@@ -1088,7 +1091,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[w]);
+        if (ok && lane == 0) mbar_arrive(&ctl->p_full[w]);
       }
       if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
       // (the streams' maxima and sums); all threads decide alike whether to go on

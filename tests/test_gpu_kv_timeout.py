@@ -40,3 +40,37 @@ def test_waits_run_out_and_the_next_call_is_right(ss, cuda_device, N, lens, grou
     out = c.attend(0, plan, q)
     assert (plan.status == 0).all()
     check_attend(c, table, q, out, lens, [N] * 3)
+
+
+def steady(ss, cuda_device, D, N, lens, group=None, H=2, Q=8):
+    shared = ([0] * len(lens), 512) if group else None
+    c, table = make(ss, cuda_device, lens, [N] * len(lens), 64, H, D, shared=shared, seed=N)
+    q = queries(len(lens), N, Q, D, torch.bfloat16, cuda_device)
+    g = i32(group, cuda_device) if group else None
+    want = c.attend(0, c.plan(N, Q, group=g), q)
+    check_attend(c, table, q, want, lens, [N] * len(lens))
+    return c, q, g, Q, want
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_giving_up_at_any_step_hands_nothing_on(ss, cuda_device, D):
+    """Limits from one that no wait meets to some that most meet, over shares of
+    many blocks: roles give up in the middle of their rings.  Every sequence that
+    keeps its status keeps its result, and the calls after are whole."""
+    from sam_drafting_verification_gb300 import _binding as bd
+    lib = bd.lib()
+    N, lens = 40, [9000, 30, 4000, 700]   # 160 rows a key head: two row tiles
+    c, q, g, Q, want = steady(ss, cuda_device, D, N, lens)
+    for ns in (1, 300, 700, 1500, 3000, 6000, 12000, 25000):
+        before = lib.kv_set_wait_limit_ns(ns)
+        try:
+            plan = c.plan(N, Q)
+            out = c.attend(0, plan, q)
+            torch.cuda.synchronize()
+        finally:
+            lib.kv_set_wait_limit_ns(before)
+        for b, st in enumerate(plan.status.tolist()):
+            assert st in (0, bd.ST_TIMEOUT)
+            if st == 0:
+                assert torch.equal(out[b], want[b]), (ns, b)
+        assert torch.equal(c.attend(0, c.plan(N, Q), q), want), ns
