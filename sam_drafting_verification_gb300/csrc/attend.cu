@@ -545,6 +545,7 @@ struct Ctl {
   uint64_t full[11], empty[11], s_full[2], p_full[2], q_full[2], q_empty[2], o_done, o_free, drain;
   uint32_t tmem;
   int32_t abort, bad;
+  int32_t asked, asked_q;  // tiles that the loader has requested, once it has ended
   float2 ml[2][128];  // running maxima and sums that the streams exchange
   alignas(16) Segment seg[4];
 };
@@ -863,11 +864,9 @@ __global__ void __launch_bounds__(384, 1)
           key0 += kKeyBlock;
         }
       }
-      // given up: what was requested has to land before the CTA may end
-      if (!ok) {
-        for (int t = qt < 2 ? 0 : qt - 2; t < qt; ++t) drain_wait(&ctl->q_full[t & 1], (t >> 1) & 1);
-        for (int t = kt < R::kStages ? 0 : kt - R::kStages; t < kt; ++t)
-          drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
+      if (lane == 0) {
+        ctl->asked = kt;
+        ctl->asked_q = qt;
       }
     } else if (warp == 9) {
       // ---- matrix products ----
@@ -936,10 +935,6 @@ __global__ void __launch_bounds__(384, 1)
           qt += rows2 ? 2 : 1;
         }
         if (ok && v_stage >= 0) product();
-        if (!ok) {
-          mma_commit(&ctl->drain);
-          drain_wait(&ctl->drain, 0);
-        }
       }
       __syncwarp();
     }
@@ -1199,6 +1194,22 @@ __global__ void __launch_bounds__(384, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (vload(&ctl->abort)) {
+    // Given up, by whichever role: no role issues any more, and what is in flight
+    // has to land before the CTA's shared and tensor memory go.  (A role cannot
+    // see to that when it ends: it may have issued its last copy or product, and
+    // met no wait that ran out, before another one gives up.)
+    if (warp == 8) {
+      const int kt = ctl->asked, qt = ctl->asked_q;
+      for (int t = max(qt - 2, 0); t < qt; ++t) drain_wait(&ctl->q_full[t & 1], (t >> 1) & 1);
+      for (int t = max(kt - R::kStages, 0); t < kt; ++t)
+        drain_wait(&ctl->full[t % R::kStages], (t / R::kStages) & 1);
+    } else if (tid == 9 * 32) {  // (the thread that has issued them)
+      mma_commit(&ctl->drain);
+      drain_wait(&ctl->drain, 0);
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 9) tmem_free(tmem, 512);
 }

@@ -74,3 +74,27 @@ def test_giving_up_at_any_step_hands_nothing_on(ss, cuda_device, D):
             if st == 0:
                 assert torch.equal(out[b], want[b]), (ns, b)
         assert torch.equal(c.attend(0, c.plan(N, Q), q), want), ns
+
+
+@pytest.mark.parametrize("D,N,lens,group", [(128, 4, [100, 50, 260], None), (64, 4, [700, 90, 1000], None),
+                                            (128, 1, [0, 3, 127], None), (128, 200, [64, 0, 900], None),
+                                            (64, 2, [600, 601, 640], [0, 0, 0])])
+def test_giving_up_with_everything_asked_for(ss, cuda_device, D, N, lens, group):
+    """Shares that fit the ring: the loader has requested all of its tiles, and met
+    no wait, before another role gives up.  What is in flight has to land in the
+    CTA that asked for it: calls that give up and calls that do not take turns on
+    the same SMs, and each of the latter is whole."""
+    from sam_drafting_verification_gb300 import _binding as bd
+    lib = bd.lib()
+    c, q, g, Q, want = steady(ss, cuda_device, D, N, lens, group)
+    for turn in range(30):
+        before = lib.kv_set_wait_limit_ns(1 + 40 * turn)
+        try:
+            plan = c.plan(N, Q, group=g)
+            c.attend(0, plan, q)
+        finally:
+            lib.kv_set_wait_limit_ns(before)
+        after = c.plan(N, Q, group=g)
+        got = c.attend(0, after, q)   # may begin as the one before ends
+        assert set(plan.status.tolist()) <= {0, bd.ST_TIMEOUT}
+        assert (after.status == 0).all() and torch.equal(got, want), turn
