@@ -81,7 +81,10 @@ class Rollout:
         finished sequence's automaton is not used again by this rollout; a
         caller that goes on with it should reset and rebuild it from the
         returned text.  With a cache, a finished sequence's row is emptied and
-        its pages are given back."""
+        its pages are given back (one whose limit is 0 takes no part: its row
+        stays as it is).  Where run raises for a sequence that the cache had no
+        room for, every row of that step stands for what it holds: the refused
+        ones as before the step, the others with the step's accepted tokens."""
         dev = self.batch.device
         B = self.batch.B
         limit = [int(x) for x in max_new_tokens]
@@ -129,8 +132,11 @@ class Rollout:
             read = n * K1 + 3 * n
             if cache is not None:
                 last = r["out_token"]
-                cache.commit(rows, r["accept_len"])
-                hostbuf[read:read + n] = plan.status
+                # of a sequence that the plan refused, or whose attention gave up,
+                # the slots hold no keys and values: nothing is kept
+                refused = plan.status
+                cache.commit(rows, torch.where(refused == 0, r["accept_len"], -1))
+                hostbuf[read:read + n] = refused
                 read += n
             h = hostbuf[:read].cpu()
             if cache is not None:

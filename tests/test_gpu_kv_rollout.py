@@ -190,3 +190,52 @@ def test_tree_step_keeps_the_accepted_path(ss, cuda_device):
             got = x[:, pg, :, at % page]
             assert torch.equal(got[:lens[b]], y[:, old, :, at[:lens[b]] % page])
             assert torch.equal(got[lens[b]:], new[:, b, nodes].transpose(0, 1))
+
+
+@pytest.mark.parametrize("K", [0, 3])
+def test_a_row_that_the_cache_refused_keeps_its_length(ss, cuda_device, K):
+    """Two sequences and no page left: the second one's pass is refused.  Its row then
+    holds what it held before, while the first one's has grown."""
+    dev, V = cuda_device, 40
+    batch = ss.SamBatch(2, 200, V, device=dev)
+    batch.extend(torch.zeros((2, 32), dtype=torch.int32, device=dev), i32([32, 32], dev))
+    cache = ss.KVCache(1, 4, 16, 1, 64, 2, 8, device=dev)
+    first = i32([20, 31], dev)
+    assert cache.reserve(None, first).tolist() == [0, 0]
+    assert cache.commit(None, first - 1).tolist() == [0, 0]      # two pages each
+    from sam_drafting_verification_gb300.rollout import Rollout
+    held = []
+
+    def model(rows, n_done, tokens, n_tok, plan):
+        held.append((cache.lens.tolist(), plan.status.tolist(), n_tok.tolist()))
+        logits = torch.zeros((len(rows), tokens.shape[1], V), device=dev)
+        logits[..., 0] = 9.0       # every draft of zeros is accepted
+        return logits
+
+    ro = Rollout(batch, model, K=K, cache=cache, q_heads=1, last=i32([0, 0], dev))
+    with pytest.raises(RuntimeError, match="sequence 1: cache status 1"):
+        ro.run([60, 60])
+    lens, status, n_tok = held[-1]
+    assert status == [0, 1]
+    assert cache.lens.tolist() == [lens[0] + n_tok[0], lens[1]]
+    assert (cache.held * 16 >= cache.lens).all()
+
+
+def test_a_shared_row_that_the_cache_refused_keeps_its_length(ss, cuda_device):
+    """Two samples of one prompt and no page left for a copy of the page that they
+    share: the slots behind the prompt are neither's, and nothing is committed."""
+    dev, V = cuda_device, 40
+    batch = ss.SamBatch(2, 200, V, device=dev)
+    batch.extend(torch.zeros((2, 9), dtype=torch.int32, device=dev), i32([9, 9], dev))
+    cache = ss.KVCache(1, 1, 16, 1, 64, 2, 4, device=dev)
+    assert cache.reserve(i32([0], dev), 8).tolist() == [0]
+    assert cache.commit(i32([0], dev), i32([7], dev)).tolist() == [0]
+    assert cache.fork(i32([0], dev), i32([1], dev)).tolist() == [0]
+    from sam_drafting_verification_gb300.rollout import Rollout
+
+    def model(rows, n_done, tokens, n_tok, plan):
+        return torch.zeros((len(rows), tokens.shape[1], V), device=dev)
+
+    with pytest.raises(RuntimeError, match="cache status 1"):
+        Rollout(batch, model, K=2, cache=cache, q_heads=1, last=i32([0, 0], dev)).run([5, 5])
+    assert cache.lens.tolist() == [8, 8] and cache.refs.tolist() == [2]
