@@ -31,10 +31,8 @@ constexpr int kCowBit = 1 << 30;
 
 // One CTA: the whole outcome hangs on prefix sums over the sequences (a few
 // thousand at most) and over the bitmap, each read once; latency is its cost.
-__global__ void __launch_bounds__(1024) reserve_kernel(KvView c, const int32_t* __restrict__ rows,
-                                                       int n, int N,
-                                                       const int32_t* __restrict__ n_tok,
-                                                       int32_t* __restrict__ status, ReserveWs w) {
+__global__ void __launch_bounds__(1024) reserve_kernel(KvView c, const int32_t* rows, int n, int N,
+                                                       const int32_t* n_tok, int32_t* status, ReserveWs w) {
   __shared__ int part[32];
   const int tid = threadIdx.x;
   wait_for_previous();
@@ -163,7 +161,7 @@ __global__ void __launch_bounds__(1024) reserve_kernel(KvView c, const int32_t* 
 
 // Filled slots of shared pages to their new pages: a warp takes one (copy,
 // layer, pool, head) at a time, filled * head_dim * 2 contiguous bytes.
-__global__ void __launch_bounds__(256) copy_pages_kernel(KvView c, const int32_t* __restrict__ cow) {
+__global__ void __launch_bounds__(256) copy_pages_kernel(KvView c, const int32_t* cow) {
   const int lane = threadIdx.x & 31;
   const int64_t per = (int64_t)c.layers * 2 * c.kv_heads;
   wait_for_previous();
@@ -194,9 +192,8 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(KvView c, const int32_t
 }
 
 // ---- fork --------------------------------------------------------------------
-__global__ void __launch_bounds__(256) fork_kernel(KvView c, const int32_t* __restrict__ src,
-                                                   const int32_t* __restrict__ dst, int n,
-                                                   int32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256) fork_kernel(KvView c, const int32_t* src, const int32_t* dst, int n,
+                                                   int32_t* status) {
   const int i = blockIdx.x, tid = threadIdx.x;
   wait_for_previous();
   let_next_start();
@@ -254,10 +251,9 @@ __global__ void __launch_bounds__(256) fork_kernel(KvView c, const int32_t* __re
 struct Judged {
   int st, row, len, new_len, held, accept, path;
 };
-__device__ __forceinline__ Judged judge(const KvView& c, const int32_t* __restrict__ rows, int n, int i,
-                                        int N, const int32_t* __restrict__ accept,
-                                        const int32_t* __restrict__ path,
-                                        const int32_t* __restrict__ new_len, int lane) {
+__device__ __forceinline__ Judged judge(const KvView& c, const int32_t* rows, int n, int i, int N,
+                                        const int32_t* accept, const int32_t* path, const int32_t* new_len,
+                                        int lane) {
   Judged j = {SAMSPEC_ST_OK, rows ? rows[i] : i, 0, 0, 0, 0, -1};
   bool twice = false;
   if (rows)
@@ -324,11 +320,9 @@ __device__ __forceinline__ Judged judge(const KvView& c, const int32_t* __restri
 // them.
 constexpr int kMoveItems = 64;
 template <int D>
-__global__ void __launch_bounds__(256) move_path_kernel(KvView c, const int32_t* __restrict__ rows,
-                                                        int n, int N,
-                                                        const int32_t* __restrict__ accept,
-                                                        const int32_t* __restrict__ path,
-                                                        int32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256) move_path_kernel(KvView c, const int32_t* rows, int n, int N,
+                                                        const int32_t* accept, const int32_t* path,
+                                                        int32_t* status) {
   constexpr int kLanes = D / 8;           // 16-byte pieces of a row
   constexpr int kRows = 32 / kLanes;      // rows at a time
   constexpr int kSteps = 32 / kRows;      // 31 rows at most
@@ -382,11 +376,9 @@ __global__ void __launch_bounds__(256) move_path_kernel(KvView c, const int32_t*
 
 // Lengths set, pages behind them released: one warp a sequence.  Of a commit
 // with a path the status is move_path_kernel's: references change here.
-__global__ void __launch_bounds__(256) set_len_kernel(KvView c, const int32_t* __restrict__ rows, int n,
-                                                      int N, const int32_t* __restrict__ accept,
-                                                      const int32_t* __restrict__ path,
-                                                      const int32_t* __restrict__ new_len,
-                                                      int32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256) set_len_kernel(KvView c, const int32_t* rows, int n, int N,
+                                                      const int32_t* accept, const int32_t* path,
+                                                      const int32_t* new_len, int32_t* status) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_for_previous();

@@ -86,6 +86,9 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 // Programmatic dependent launch: a kernel may be started while the one before
 // it in the stream still runs; nothing that one writes, or may still read, is
 // touched before wait_for_previous().  (Launch gaps of about 2 us a kernel.)
+// So the arguments of such kernels carry no __restrict__: with const it promises
+// that what they point to does not change while the kernel runs, and allows loads
+// that are not coherent, or moved before the wait.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... A, typename... B>

@@ -318,3 +318,15 @@ def test_a_cache_outside_the_limits_is_refused_when_made(monkeypatch, page, D, m
         ss.KVCache.wrap(k, k, *tensors)
     good = torch.zeros((1, 2, 1, 16, 64), dtype=torch.bfloat16)
     assert ss.KVCache.wrap(good, good, i32(1, 3), *tensors[1:]).page == 16
+
+
+def test_kernels_that_begin_early_promise_no_constant_inputs():
+    """With programmatic dependent launch a kernel is resident while the one before
+    it still writes what this one reads after its wait: `const __restrict__` would
+    say that it does not change meanwhile."""
+    csrc = os.path.join(ROOT, "sam_drafting_verification_gb300", "csrc")
+    for f in ("attend.cu", "cache.cu", "kv.cuh"):
+        src = re.sub(r"//.*", "", open(os.path.join(csrc, f)).read())
+        assert "wait_for_previous()" in src
+        for promise in ("__restrict__", "__ldg(", "ld.global.nc"):
+            assert promise not in src, (f, promise)
