@@ -117,7 +117,7 @@ __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int la
     }
     if (__any_sync(kFullMask, bad)) st = SAMSPEC_ST_PAGE;
     else if (__any_sync(kFullMask, lent)) st = SAMSPEC_ST_CAPACITY;
-    if (st == SAMSPEC_ST_OK && P.group) {
+    if (st == SAMSPEC_ST_OK && P.group && nt > 0) {
       const int g = P.group[i];
       for (int k = i - 1; k >= 0; k -= 32) {
         const int j = k - lane;
@@ -128,15 +128,32 @@ __device__ __forceinline__ void plan_sequence(const PlanParams& P, int i, int la
         }
         leader = k - 31;
       }
+      // The first of them that may take part, as far as its counts say: one
+      // without tokens, or whose row is empty by now, has no pages to share.
+      // (Where that one is refused for its table or its tree, what follows holds
+      // all the same: equal entries of this sequence's own checked table.)
+      for (int k0 = leader; k0 < i; k0 += 32) {
+        const int j = k0 + lane;
+        bool may = j >= i;
+        if (!may) {
+          const int r = P.rows ? P.rows[j] : j, t = P.first_child ? P.N : P.n_tok ? P.n_tok[j] : P.N;
+          if (r >= 0 && r < c.seqs && t > 0 && t <= P.N) {
+            const int b = c.lens[r], held = c.held[r];
+            may = b >= 0 && held >= 0 && held <= c.max_pages && (int64_t)held << c.log_page >= (int64_t)b + t;
+          }
+        }
+        const uint32_t found = __ballot_sync(kFullMask, may);
+        leader = i;
+        if (found) {
+          leader = min(k0 + __ffs(found) - 1, i);
+          break;
+        }
+      }
       if (leader != i) {
         const int lrow = P.rows ? P.rows[leader] : leader;
-        int lfull = 0;
-        if (lrow >= 0 && lrow < c.seqs) {
-          const int ll = c.lens[lrow];
-          lfull = ll > 0 ? min(ll >> c.log_page, c.max_pages) : 0;
-        }
+        const int lfull = c.lens[lrow] >> c.log_page;
         const int m = min(full, lfull);
-        const int32_t* tl = c.table + (int64_t)(m ? lrow : 0) * c.max_pages;
+        const int32_t* tl = c.table + (int64_t)lrow * c.max_pages;
         int same = m;
         for (int k0 = 0; k0 < m && same == m; k0 += 128) {
           bool d[4];
@@ -208,25 +225,36 @@ __global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P, bool 
   const int tt = tile_tokens(P.rep);
   KvSeq* seq = P.plan.seq;
   if (P.group) {
+    // only members that take part count: the others bring no rows, set no limit
+    // and take none away from those behind them
+    for (int i = tid; i < n; i += 1024) {
+      seq[i].shared = 0x7fffffff;
+      seq[i].gsize = 0;
+      seq[i].first = 0x7fffffff;
+    }
+    __syncthreads();
     for (int i = tid; i < n; i += 1024)
-      if (seq[i].ntok > 0 && seq[i].leader == i) {
-        seq[i].shared = seq[i].lcp;
-        seq[i].gsize = 1;
+      if (seq[i].ntok > 0) {
+        KvSeq& led = seq[seq[i].leader];
+        atomicMin(&led.shared, seq[i].lcp);
+        atomicMax(&led.gsize, i - seq[i].leader + 1);
+        atomicMin(&led.first, i);
       }
     __syncthreads();
+    // what two or more share, from a length on
     for (int i = tid; i < n; i += 1024)
-      if (seq[i].leader != i) {
-        // the group's extent counts every member; those without new tokens
-        // bring no rows and set no limit
-        atomicMax(&seq[seq[i].leader].gsize, i - seq[i].leader + 1);
-        if (seq[i].ntok > 0) atomicMin(&seq[seq[i].leader].shared, seq[i].lcp);
+      if (seq[i].leader == i && (seq[i].first == i + seq[i].gsize - 1 || seq[i].shared < kMinShared)) seq[i].shared = 0;
+    __syncthreads();
+    // the first that takes part leads, where the one that the pages were compared
+    // with was refused
+    for (int i = tid; i < n; i += 1024)
+      if (seq[i].ntok > 0) {
+        const int led = seq[i].leader, first = seq[led].first;
+        seq[i].leader = first;
+        if (i == led) continue;
+        seq[i].shared = seq[led].shared;
+        if (i == first) seq[i].gsize = seq[led].gsize - (first - led);
       }
-    __syncthreads();
-    for (int i = tid; i < n; i += 1024)
-      if (seq[i].leader == i && (seq[i].gsize < 2 || seq[i].shared < kMinShared)) seq[i].shared = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += 1024)
-      if (seq[i].leader != i) seq[i].shared = seq[i].ntok > 0 ? seq[seq[i].leader].shared : 0;
     __syncthreads();
   }
   // tiles of the groups' shared keys, then of each sequence's own; the costs
@@ -268,7 +296,7 @@ __global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P, bool 
       if (i < n) {
         q = seq[i];
         if (own) cnt = (q.ntok + 2 * tt - 1) / (2 * tt);
-        else if (q.leader == i && q.shared > 0) cnt = (q.gsize * P.N + 2 * tt - 1) / (2 * tt);
+        else if (q.ntok > 0 && q.leader == i && q.shared > 0) cnt = (q.gsize * P.N + 2 * tt - 1) / (2 * tt);
       }
       auto cost_of = [&](const KvTile& t) { return (t.blocks * block_cost(t) + unit_cost(t)) * c.kv_heads; };
       for (int k = sub; k < cnt; k += lanes) sum += cost_of(tile_of(q, i, k, own));

@@ -113,11 +113,11 @@ struct KvSeq {
   int32_t row;     // its row in the cache
   int32_t base;    // committed tokens
   int32_t ntok;    // new tokens (0: a status is set)
-  int32_t leader;  // first sequence of its group
-  int32_t lcp;     // tokens of the pages that it shares with the leader
-  int32_t shared;  // tokens that its group reads once (0: none; at every member)
-  int32_t gsize;   // the group's sequences (at the leader)
-  int32_t pad;
+  int32_t leader;  // first sequence of its group that takes part (itself: none, or it takes none)
+  int32_t lcp;     // tokens of the pages that it shares with the first that might
+  int32_t shared;  // tokens that its group reads once (0: none; at every member that takes part)
+  int32_t gsize;   // at the leader: sequences up to the last that takes part
+  int32_t first;   // (of the plan's own)
 };
 // a unit of attention work, once for each key head: the queries of `toks`
 // tokens (tokens of consecutive sequences follow one another, rep query heads
