@@ -219,12 +219,13 @@ class KVCache:
     def reserve(self, rows, n_tok, out=None):
         """Room for n_tok more tokens (int32 [n], or one number) behind the
         committed ones of sequences `rows` (int32 [n], or None for all).  Returns
-        the status words int32 [n]: ST_CAPACITY where pages ran out."""
+        the status words int32 [n]: ST_CAPACITY where pages ran out, or the
+        sequence would be longer than its table."""
         if isinstance(n_tok, torch.Tensor):
             if n_tok.dim() != 1:
                 raise ValueError("n_tok must be [n]")
             n, rp = self._rows(rows, n_tok.shape[0])
-            most, np = min(self.max_pages * self.page, 1 << 30), self._i32(n_tok, "n_tok", (n,))
+            most, np = 1 << 30, self._i32(n_tok, "n_tok", (n,))   # (the call's limit, past any cache's)
         else:
             n, rp = self._rows(rows)
             most, np = max(-1, min(int(n_tok), (1 << 31) - 1)), None   # (the call takes 32 bits)

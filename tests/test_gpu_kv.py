@@ -655,6 +655,18 @@ def test_the_same_row_twice_changes_nothing(ss, cuda_device):
     assert c.held.tolist() == [0, 1, 0, 0]
 
 
+def test_reserving_more_than_the_table_holds(ss, cuda_device):
+    dev = cuda_device
+    c = ss.KVCache(1, 20, 16, 1, 64, 3, 6, device=dev)
+    for ask in ([96, 97, 5], [3, 10 ** 6, 1 << 30], [1, (1 << 30) + 1, -1]):
+        want = [1 if 96 < x <= 1 << 30 else ref.ST_BADDRAFT if not 0 <= x <= 1 << 30 else 0 for x in ask]
+        assert c.reserve(None, i32(ask, dev)).tolist() == want
+        if max(ask) <= 1 << 30 and min(ask) >= 0:
+            assert want == ref.Pages(20, 16, 3, 6).reserve([0, 1, 2], ask)
+    assert c.reserve(None, 97).tolist() == [1, 1, 1]
+    assert c.held.tolist() == [6, 0, 1]
+
+
 def test_many_sequences_and_a_large_pool(ss, cuda_device):
     """More sequences than a block of threads, a bitmap of several rounds, pages
     taken behind a long run of others' pages."""

@@ -330,3 +330,12 @@ def test_kernels_that_begin_early_promise_no_constant_inputs():
         assert "wait_for_previous()" in src
         for promise in ("__restrict__", "__ldg(", "ld.global.nc"):
             assert promise not in src, (f, promise)
+
+
+def test_reserve_judges_a_tensor_as_it_does_a_number(cache):
+    """More tokens than the table holds are too many (ST_CAPACITY), not a bad
+    number, however they are given."""
+    for ask in (i32(2), 5000):
+        cache.rec.calls.clear()
+        cache.reserve(i32(2), ask)
+        assert all(a[3] >= 5000 for n, a in cache.rec.calls if n == "kv_reserve")
