@@ -313,11 +313,19 @@ class KVCache:
         self._call("kv_plan", rp, n, N, q_heads, np, fp, sp, gp, out.ptr, out.bytes)
         return out
 
+    def _capturing(self):
+        """Is the stream that the calls go to (the cache's device's, which need not
+        be the current one) being captured in a graph?"""
+        if torch.cuda.device_count() > 1 and torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return torch.cuda.is_current_stream_capturing()
+        return torch.cuda.is_current_stream_capturing()
+
     def _new_plan(self, n, N, q_heads, grouped, need):
         # memory of a plan that is gone, if one of about this size was used on
         # this stream; not inside a graph capture, whose graph keeps its own
         spare = buf = None
-        if self.device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        if self.device.type == "cuda" and not self._capturing():
             spare = self._spare.setdefault(_pkg._raw_stream(self.device.index), [])
             try:
                 for _ in range(2):   # taken out before it is looked at: another thread may do the same

@@ -339,3 +339,47 @@ def test_reserve_judges_a_tensor_as_it_does_a_number(cache):
         cache.rec.calls.clear()
         cache.reserve(i32(2), ask)
         assert all(a[3] >= 5000 for n, a in cache.rec.calls if n == "kv_reserve")
+
+
+class _Block:
+    def __init__(self, size):
+        self.size = size
+
+    def numel(self):
+        return self.size
+
+    def data_ptr(self):
+        return P
+
+
+@pytest.mark.parametrize("current,capturing", [(0, {0}), (1, {0}), (0, {1}), (1, {1}), (1, set())])
+def test_capture_is_asked_of_the_caches_own_device(cache, monkeypatch, current, capturing):
+    """With another device current, a plan that is captured neither takes spare
+    memory nor gives its own back, and one that is not does both."""
+    now = [current]
+
+    class Device:
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def __enter__(self):
+            now.append(self.device.index)
+
+        def __exit__(self, *exc):
+            now.pop()
+
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[-1] in capturing)
+    monkeypatch.setattr(ss, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch, "empty", lambda n, **kw: _Block(n))
+    monkeypatch.setattr(cache, "device", torch.device("cuda", 0))
+    old = _Block(4096)
+    spare = cache._spare[0] = [old]
+    plan = cache._new_plan(2, 3, 4, False, 4096)
+    assert now == [current]
+    assert (plan.buf is old) == (0 not in capturing)
+    mine = plan.buf
+    del plan
+    assert (mine in spare) == (0 not in capturing)
