@@ -27,6 +27,11 @@ from . import _cuda_device, _req
 
 _pkg = sys.modules[__package__]
 _DTYPES = {torch.bfloat16: _b.BF16, torch.float16: _b.F16}
+# Memory of a plan that is gone is kept for the next one up to this size (two of
+# them a stream): it saves some 5 us of host time a plan.  Plans beyond it, of long
+# prompts or large groups, work for far longer than that, and their memory returns
+# to torch's allocator.
+_SPARE_BYTES = 64 << 20
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -323,9 +328,10 @@ class KVCache:
 
     def _new_plan(self, n, N, q_heads, grouped, need):
         # memory of a plan that is gone, if one of about this size was used on
-        # this stream; not inside a graph capture, whose graph keeps its own
+        # this stream (and is small enough to be kept); not inside a graph capture,
+        # whose graph keeps its own
         spare = buf = None
-        if self.device.type == "cuda" and not self._capturing():
+        if need <= _SPARE_BYTES and self.device.type == "cuda" and not self._capturing():
             spare = self._spare.setdefault(_pkg._raw_stream(self.device.index), [])
             try:
                 for _ in range(2):   # taken out before it is looked at: another thread may do the same

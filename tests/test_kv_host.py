@@ -383,3 +383,19 @@ def test_capture_is_asked_of_the_caches_own_device(cache, monkeypatch, current, 
     mine = plan.buf
     del plan
     assert (mine in spare) == (0 not in capturing)
+
+
+def test_large_plans_give_their_memory_back_to_torch(cache, monkeypatch):
+    """What a cache holds on to for its next plans is bounded, whatever was planned."""
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(ss, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch, "empty", lambda n, **kw: _Block(n))
+    monkeypatch.setattr(cache, "device", torch.device("cuda", 0))
+    for need in (4096, 1 << 20, 1 << 30, 64 << 20, 200 << 20, 1 << 34):
+        plan = cache._new_plan(2, 3, 4, False, need)
+        assert plan.buf.numel() >= need
+        del plan
+        assert sum(x.numel() for x in cache._spare.get(0, [])) <= 2 * (64 << 20)
+    small = cache._new_plan(2, 3, 4, False, 64 << 20)   # (what was kept last, still there)
+    assert small.buf.numel() == 64 << 20 and cache._spare[0] == []
