@@ -24,7 +24,7 @@ struct PlanParams {
   const int32_t* first_child;
   const int32_t* next_sibling;
   const int32_t* group;
-  int n, N, q_heads, rep;
+  int n, N, rep;
 };
 
 // A warp: its sequence's lengths and pages checked, the tree's depths and
@@ -374,11 +374,9 @@ __global__ void __launch_bounds__(1024, 1) plan_units_kernel(PlanParams P, bool 
   // CTAs without a share begin where the last one ends
   for (int x = ctas + 1 + tid; x <= kKvCtas; x += 1024) P.plan.start[x] = {tiles, 0, 0, 0};
   if (tid == 0) {
-    P.plan.hdr[kHdrTiles] = tiles;
     P.plan.hdr[kHdrCtas] = ctas;
     P.plan.hdr[kHdrCost] = cost;
     P.plan.hdr[kHdrTree] = P.first_child != nullptr;
-    P.plan.hdr[kHdrTimeout] = 0;
   }
 }
 
@@ -807,8 +805,12 @@ __global__ void __launch_bounds__(384, 1)
   unsigned char* ring = smem + 2 * R::kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const KvView& c = P.c;
-  if (smem_u32(smem) & 1023) {  // the swizzle counts from there; the linker sees to it
-    if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
+  if (smem_u32(smem) & 1023) {
+    // The swizzle counts from there, and the linker sees to it.  Were it not so,
+    // nothing is computed, and every sequence says so.
+    wait_for_previous();
+    let_next_start();
+    for (int i = blockIdx.x * 384 + tid; i < P.n; i += kKvCtas * 384) P.plan.status[i] = SAMSPEC_ST_TIMEOUT;
     return;
   }
   if (warp == 9) tmem_alloc(&ctl->tmem, 512);
@@ -1217,7 +1219,6 @@ __global__ void __launch_bounds__(384, 1)
           const int end = (wk.t.tok0 + wk.t.toks - 1) / P.N;
           for (int j = wk.t.tok0 / P.N + tid; j <= end; j += 256) P.plan.status[j] = SAMSPEC_ST_TIMEOUT;
         }
-      if (tid == 0) P.plan.hdr[kHdrTimeout] = 1;
     }
   }
   tc_fence_before();
@@ -1536,7 +1537,6 @@ int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, 
   P.group = d_group;
   P.n = n;
   P.N = N;
-  P.q_heads = q_heads;
   P.rep = q_heads / P.c.kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // up to 32 sequences, a warp each, are judged by the units' CTA: one launch

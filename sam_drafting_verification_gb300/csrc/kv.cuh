@@ -143,7 +143,7 @@ struct KvJoin {
   int32_t pad[2];
 };
 inline __host__ __device__ int tile_tokens(int rep) { return kRows / rep; }
-enum { kHdrTiles = 0, kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrTimeout = 4, kHdrInts = 16 };
+enum { kHdrCtas = 1, kHdrCost = 2, kHdrTree = 3, kHdrInts = 16 };
 
 struct PlanLayout {
   size_t status, hdr, seq, node, suf0, pre0, tile, start, join, ml, o, bytes;
