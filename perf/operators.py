@@ -431,7 +431,7 @@ def _run_own(st):
     kind = c["kind"]
     if "cache" not in st:   # the handle that a program keeps for its cache and its positions
         st["cache"] = ss.KVCache.wrap(*(st[x] for x in ("k", "v", "table", "lens", "held", "refs", "free")))
-        st["rope"] = ss.Rope(st["inv_freq"], c["layout"], st["mscale"]) if c["rot"] else None
+        st["rope"] = ss.Rope(st["inv_freq"], c["layout"], st["mscale"]) if "inv_freq" in st else None
     cache, rope = st["cache"], st["rope"]
     if kind == "fork":
         cache.truncate(rows, st["zero"])
