@@ -73,7 +73,8 @@ typedef struct kv_cache {
  * free pages is gone, or whose table row is too short, gets ST_CAPACITY (so
  * does each later one that needs more pages than are left after those before
  * it).  Where the last page is partly filled and held by others too, its
- * filled slots are copied to a page of the sequence's own, in all layers.
+ * filled slots are copied to a page of the sequence's own, in all layers
+ * (whatever n_tok[i] is, 0 included).
  * Workspace: kv_reserve_workspace_bytes bytes, 16-byte aligned, any content,
  * not shared by two calls in flight.  Two launches. */
 size_t kv_reserve_workspace_bytes(const kv_cache* cache, int32_t n);
@@ -114,7 +115,8 @@ int kv_truncate(const kv_cache* cache, const int32_t* d_rows, int32_t n,
  * ancestors.  Its position is lens + j, or lens + depth.  d_group [n] (may be
  * NULL): consecutive sequences of the same number form a group; the pages
  * that the table rows of all its sequences begin with are read once for the
- * whole group.  Grouping changes no result beyond rounding.  Slots must have
+ * whole group (sequences without tokens, or with a status, count for nothing in
+ * it).  Grouping changes no result beyond rounding.  Slots must have
  * been reserved (ST_CAPACITY).  d_plan: kv_plan_bytes bytes, 256-byte
  * aligned, any content; it starts with the n status words, and holds the
  * workspace of kv_attend: one kv_attend at a time may use a plan (grouped:
@@ -123,8 +125,14 @@ int kv_truncate(const kv_cache* cache, const int32_t* d_rows, int32_t n,
  * a cache of the same sizes (but for layers and n_pages) and table.  A plan holds until
  * the cache's lengths or tables change.  Limits: n <= 2^20, N <= 2^16, q_heads
  * a multiple of kv_heads, at most 64 times as many, n * N * q_heads < 2^30
- * (with groups 2^29), and units of work times key blocks below 2^31 (a call
- * of some 2000 sequences of a million tokens each and 8 key heads). */
+ * (with groups 2^29), and what the units of work may cost below 2^31: units *
+ * ((max_pages * page / 128 + 2) * 2 + 5) * kv_heads, by the table's width,
+ * however short the sequences are.  A unit is up to 2 * floor(128 / rep) tokens
+ * of a sequence, rep = q_heads / kv_heads; with groups ceil(n * N / those) + n
+ * units more count.  (Tables of a million tokens and 8 key heads: 16,000
+ * sequences of one unit each, 8,000 with groups.)  A grouped plan holds two fp32
+ * results of every query row besides, 2 * n * N * q_heads * (4 * head_dim + 8)
+ * bytes: 1 GB for 8 sequences of 4000 tokens and 32 heads of 128. */
 size_t kv_plan_bytes(const kv_cache* cache, int32_t n, int32_t N, int32_t q_heads,
                      int32_t grouped);
 int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, int32_t q_heads,
@@ -156,7 +164,8 @@ int kv_append(const kv_cache* cache, int32_t layer, const void* d_plan, int32_t 
  * scale positive and finite.
  * Scores, softmax and sums in fp32; the probabilities are rounded to the
  * cache's dtype for the product with v.  Keys and values outside a token's
- * sight never reach it, whatever they hold (infinities and NaN included).
+ * sight never reach it, whatever they hold (infinities and NaN included).  A
+ * query all of whose scores are -infinity gets zeros.
  * Tokens beyond n_tok, or of a sequence with a status, get zeros. */
 int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_bytes, int32_t n,
               int32_t N, int32_t q_heads, const void* d_q, int64_t q_stride, float scale,
@@ -166,8 +175,9 @@ int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_by
  * the verification kernels': every on-chip wait gives up after `ns`
  * nanoseconds (0: the default 2 s).  A kernel whose wait runs out sets
  * ST_TIMEOUT in the plan's status of the sequences that it was working on (their outputs
- * are undefined), waits for its copies and matrix products in flight (up to
- * 2 s each) and returns; the context stays usable.  Process-wide, for launches
+ * are undefined), waits for its copies and matrix products in flight (all of
+ * them, whichever wait ran out; up to 2 s each) and returns; the context stays
+ * usable.  Process-wide, for launches
  * after the call.  Returns the previous limit. */
 uint64_t kv_set_wait_limit_ns(uint64_t ns);
 

@@ -93,7 +93,8 @@ class KVPlan:
     sequence (0: takes part), and the device memory that kv_append and
     kv_attend read and work in (of the cache that made it, or one of the same
     sizes and table).  It belongs to the stream that it was made on:
-    where another one reads it, keep the plan until that one is done."""
+    where another one reads it, keep the plan until that one is done, and where a
+    graph was captured with it, as long as that is replayed."""
 
     def __init__(self, n, N, q_heads, grouped, buf, nbytes, sizes, spare=None):
         self.sizes = sizes   # of the cache: what it holds are that one's rows and pages
@@ -292,7 +293,8 @@ class KVCache:
         (int32 [n], or None for all): n_tok int32 [n] of them, a chain (None: N),
         or tree=(first_child, next_sibling) int32 [n, N] as for spec_verify_tree.
         group int32 [n]: consecutive sequences of one number read the pages
-        that they share once.  out: the plan of an earlier call with the same
+        that they share once (those without tokens, or with a status, count for
+        nothing).  out: the plan of an earlier call with the same
         sizes, written again in place."""
         N, q_heads = int(N), int(q_heads)
         n, rp = self._rows(rows)

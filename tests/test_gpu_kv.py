@@ -284,6 +284,35 @@ def test_what_no_token_sees_does_not_reach_it(ss, cuda_device, fill, N):
         assert out[b, n_tok[b] - 1, :, 50:].isfinite().all()
 
 
+@pytest.mark.parametrize("D,N,lens", [(64, 1, [0, 1, 129]), (128, 5, [700, 5000, 130]), (128, 90, [3, 260, 9])])
+@pytest.mark.parametrize("group", [None, [0, 0, 0]])
+def test_scores_of_minus_infinity(ss, cuda_device, D, N, lens, group):
+    """Keys that score -infinity take no weight, in blocks of nothing else too; a
+    query that sees no other gets zeros."""
+    dev = cuda_device
+    shared = (group, 2 * 64) if group else None
+    c, table = make(ss, dev, lens, [N] * 3, 64, 1, D, shared=shared, seed=9)
+    q = queries(3, N, 4, D, BF16, dev).abs() + 0.25
+    g = i32(group, dev) if group else None
+    c.k.abs_()
+    c.k[..., 0] = -math.inf
+    plan = c.plan(N, 4, group=g)
+    assert (c.attend(0, plan, q) == 0).all()
+    # the last 3 tokens of each history, and the new ones, are seen by score
+    for b in range(3):
+        for t in range(max(0, lens[b] - 3), lens[b] + N):
+            c.k[0, table[b, t // 64], :, t % 64, 0] = 0.5
+    out = c.attend(0, plan, q)
+    u = half_step(BF16)
+    for b in range(3):
+        k, v = gathered(c, table, 0, b, lens[b] + N)
+        keep = torch.isfinite(k[:, 0, 0])
+        base = int(keep[:lens[b]].sum())
+        o, mag, e = ref.attend(q[b], k[keep], v[keep], base, np.tril(np.ones((N, N), bool)), 1 / math.sqrt(D))
+        e = e + 2 * (lens[b] + N) * 2.0 ** -23   # (sums over the others' zeros too)
+        assert ((out[b].double() - o).abs() <= u * o.abs() + (u + e) * mag + 2.0 ** -24).all()
+
+
 @pytest.mark.parametrize("fill", [math.nan, math.inf])
 def test_siblings_do_not_see_each_other(ss, cuda_device, fill):
     rng = np.random.default_rng(4)

@@ -399,3 +399,30 @@ def test_large_plans_give_their_memory_back_to_torch(cache, monkeypatch):
         assert sum(x.numel() for x in cache._spare.get(0, [])) <= 2 * (64 << 20)
     small = cache._new_plan(2, 3, 4, False, 64 << 20)   # (what was kept last, still there)
     assert small.buf.numel() == 64 << 20 and cache._spare[0] == []
+
+
+@pytest.mark.parametrize("pages,page,heads", [(1 << 14, 64, 8), (1 << 20, 16, 3), (300, 128, 1024)])
+@pytest.mark.parametrize("N,rep", [(1, 4), (200, 4), (7, 33)])
+def test_the_limit_of_a_plans_work_is_the_one_stated(pages, page, heads, N, rep):
+    """units * ((max_pages * page / 128 + 2) * 2 + 5) * kv_heads < 2^31"""
+    lib = bd.lib()
+    tokens = 2 * (128 // rep)
+    each = ((pages * page // 128 + 2) * 2 + 5) * heads
+    d = desc(max_pages=pages, page=page, kv_heads=heads, n_pages=64, seqs=1 << 20)
+    for grouped in (0, 1):
+        units = lambda n: n * -(-N // tokens) + (-(-n * N // tokens) + n if grouped else 0)  # noqa: E731
+        n = 1
+        while units(n + 1) * each < 1 << 31 and n < 1 << 20:
+            n += 1
+        most = ((1 << 29 if grouped else 1 << 30) - 1) // (N * rep * heads)
+        n = min(n, most)
+        assert lib.kv_plan_bytes(d, n, N, rep * heads, grouped) > 0
+        assert lib.kv_plan_bytes(d, n + 1, N, rep * heads, grouped) == 0
+
+
+@pytest.mark.parametrize("n,N,Q", [(8, 4001, 32), (3, 5, 8)])
+def test_a_grouped_plan_holds_two_results_of_every_row(n, N, Q):
+    lib = bd.lib()
+    one, two = (lib.kv_plan_bytes(desc(kv_heads=8), n, N, Q, g) for g in (0, 1))
+    results = 2 * n * N * Q * (4 * 128 + 8)
+    assert results <= two - one <= 1.02 * results + (64 << 20)
