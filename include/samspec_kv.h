@@ -223,10 +223,13 @@ int kv_read(const kv_cache* cache, int32_t layer, const int32_t* d_rows, int32_t
  * (q_heads / kv_heads)), scale positive and finite.
  * Scores, softmax and sums in fp32; the probabilities are rounded to the
  * cache's dtype (or io_dtype) for the product with v.  A cache of 8 bits with no
- * groups and N * q_heads / kv_heads <= 32: as precisely, but a product of a
- * probability and its value's scale is off by up to 2^-18 (F16: 2^-20) of the row's
- * largest such product, and an element of a query by up to 2^-21 (2^-25) of the
- * largest of its head; a query with an element that is not finite gets NaN.
+ * groups and N * q_heads / kv_heads <= 32: so are products of a probability and its
+ * value's scale, but small ones to multiples of 2^-17 (F16: 2^-19) of the row's
+ * largest such product, or of 2^-21 (2^-23) where a key exceeds those about it by 2^8: up
+ * or down, as a number says that runs evenly through such a step from key to key,
+ * so with a mean of zero: n keys' errors add up to about sqrt(n) of one.  An element of a
+ * query is off by up to 2^-21 (2^-25) of the largest of its head; a query with an
+ * element that is not finite gets NaN.
  * Keys and values outside a token's
  * sight never reach it, whatever they hold (infinities and NaN included).  A
  * query all of whose scores are -infinity gets zeros.

@@ -15,14 +15,29 @@ namespace {
 // of parts: x = x0 + x1 / 16 (+ x2 / 256), each the nearest code to 16 times what is
 // left by the one before.  Two parts are a bf16 number, three an fp16 one, exactly but
 // for half a step of the last part, 2^-14 (2^-18), where a head's largest has a code of
-// at least 224.  Parts are columns of their own, added up in fp32.  Weights are rounded
-// so too: off by 2^-8 (2^-11 in fp16, as they pass through it) of themselves, or that
-// half step, 2^-18 (2^-20) of the largest so far, each times its value's scale.
+// at least 224.  Parts are columns of their own, added up in fp32.
+//
+// Weights (times their value's scale) become parts too, each off by 2^-8 (2^-11 in fp16,
+// as they pass through it) of itself; or, of small ones, by what the last part's smallest
+// step leaves, 2^-13 (2^-17).  Were small weights rounded to the nearest, all keys with
+// like scores would be off the same way, and their errors add up while the sum that
+// divides has them in full: one key with 2^20 times the weight of 131072 others, and
+// those came out 11% short.  So a number that runs evenly through a step from key to key
+// is added before the last rounding (in place of the product that it follows, a fused one:
+// no instruction), and another before that to fp16, whose smallest step is 2^-24: each
+// weight goes up as often as it has parts of a step, and errors of n keys add up like
+// sqrt(n) of them, without a direction.
 //
 // A thread has a key: the key's two scales are its own, its scores are R numbers.
 // Weights are 2^(s + c) for a row's reference c, moved only when a weight would pass
 // 2^8.5: then (all rows for the first block, later single ones) the warpgroup takes
-// those rows' maxima, and what is there is scaled.  Else a step needs one vote of 128
+// those rows' maxima, and what is there is scaled.  Where they are put: high, and small
+// weights have more steps left; low, and fewer maxima to come move the reference (2500
+// clocks: 64 sequences of 4096 keys, 32 rows of random queries: always at 2^8 222 us a call,
+// at 2^6 169, at 2^4 150; fp16 over 16k to 32k keys 232 at 2^8, 197 at 2^6, 159 at 2^4,
+// 140 at 2^2).  A row whose four warps' maxima lie together has many keys to share its
+// weight, and can have it low; where they lie apart one key may have all of it, few are
+// still to exceed it, and it goes high.  Else a step needs one vote of 128
 // threads.  The values' scale multiplies the weights on their way to the product, not
 // those of the sum.
 //
@@ -41,6 +56,7 @@ namespace {
 // block at 10 instructions each: half of the issue slots are taken, and a warp that
 // could issue waits for its instructions as often as not (the loops' code is 30 KB).
 constexpr float kReach = 8.5f;  // log2 of the largest weight (e4m3 has 448)
+constexpr float kEven = 4.f;    // how far apart (log2) maxima of 32 keys may lie for a reference put low
 constexpr int kMaxStages = 12;
 
 struct FewRow {
@@ -69,10 +85,8 @@ template <typename T, int D, int R>
 struct Few {
   static constexpr int kParts = Type16<T>::kFormat == 1 ? 2 : 3;
   static constexpr int kCols = kParts * R;  // columns of both products
-  // log2 of a row's largest weight when its reference is set: what it may grow by before that
-  // moves, taken from the smallest weights.  (fp16, 64-wide heads over 16k-32k keys, scores of
-  // standard deviation 2: 4 157 us, 3 145, 2 137, 0 136; bf16, 4096 keys: no difference.)
-  static constexpr float kTop = kParts == 2 ? 4.f : 2.f;
+  // log2 of a row's largest weight when its reference is set
+  static constexpr float kTopLow = kParts == 2 ? 4.f : 2.f, kTopHigh = 8.f;
   static_assert(R == 16 || R == 32, "a row a bit, a lane's sum");
   static constexpr int kS = 512 / kCols - 2 < 4 ? 512 / kCols - 2 : 4;  // places of scores, and of weights
   static constexpr int kTile = 128 * D, kScales = 2 * kKeyBlock;
@@ -148,12 +162,21 @@ __device__ __forceinline__ uint32_t code_values(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
-// 16 times what a pair of codes leaves of a pair (exact)
-__device__ __forceinline__ uint32_t left16(uint32_t h, uint16_t c) {
+// 16 times what a pair of codes leaves of a pair (exact), and `more` besides
+__device__ __forceinline__ uint32_t left16(uint32_t h, uint16_t c, uint32_t more) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(code_values(c)));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4c004c00u));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(r), "r"(0x4c004c00u), "r"(more));
   return r;
+}
+// What key `th` of a unit's block b adds to a weight before it is rounded: of a step of
+// size 1 a number in (-1/2, 1/2), 11 bits and none of them 1/2, so that a weight of zero
+// stays one.  A block's 128 keys have 128 numbers evenly apart, in an order (by `turn`, odd)
+// in which any few neighbours lie well apart too, and all move on from block to block (by
+// `shift`).  The two that a weight meets go by 1 / g and 1 / g^2, g^3 = g + 1, of 128 and of
+// 2^16, whose multiples fill a square evenly, not only a line.
+__device__ __forceinline__ float dither(int th, int b, uint32_t turn, uint32_t shift) {
+  return (float)(int)(((uint32_t)th * (turn << 9) + (uint32_t)b * shift) >> 5 & 2047) * 0x1p-11f - 0.5f + 0x1p-12f;
 }
 
 // Values of key `row` of a block that not every query sees: zeros where it is no key of
@@ -535,6 +558,9 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t mS = tmem + at * F::kCols + lanes;
         unsigned char* pw = smem + F::kP0 + at * F::kP + th * 16;
         const uint64_t ks2 = pack2(ks, ks), vs2 = pack2(vs, vs), part2 = pack2(0.0625f, 0.0625f);
+        const float d_half = dither(th, b, 73, 37345) * 0x1p-24f, d_code = dither(th, b, 97, 49471) * 0x1p-9f;
+        const uint64_t by_half = pack2(d_half, d_half);
+        const uint32_t by_code = half_pair(d_code, d_code);
         float s[R];
         float mx = -INFINITY;
 #pragma unroll
@@ -598,10 +624,13 @@ __global__ void __launch_bounds__(512, 1)
           if (th < 32) {
             bool move = false;
             if (lane < R) {
-              const float m =
-                  fmaxf(max3(ctl->red[w][0][lane], ctl->red[w][1][lane], ctl->red[w][2][lane]), ctl->red[w][3][lane]);
+              float a[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a[k] = ctl->red[w][k][lane];
+              const float m = fmaxf(max3(a[0], a[1], a[2]), a[3]);
               move = m > -INFINITY && (((unset >> lane) & 1) || m > kReach);
-              const float by = move ? F::kTop - m : 0.f;
+              const float apart = m - fminf(fminf(a[0], a[1]), fminf(a[2], a[3]));
+              const float by = move ? fminf(F::kTopLow + fmaxf(apart - kEven, 0.f), F::kTopHigh) - m : 0.f;
               // (a row that is set for the first time has no earlier weights)
               ctl->move[w][lane] = ex2_approx(fminf(by, 0.f));
               ctl->by[w][lane] = by;
@@ -660,14 +689,14 @@ __global__ void __launch_bounds__(512, 1)
             const float2 sum = unpack2(add2(pack2(l[i + e], l[i + e + 1]), ab));
             l[i + e] = sum.x;
             l[i + e + 1] = sum.y;
-            const float2 z = unpack2(mul2(ab, vs2));
+            const float2 z = unpack2(fma2(ab, vs2, by_half));
             uint32_t h = half_pair(z.x, z.y);
 #pragma unroll
             for (int p = 0; p < F::kParts; ++p) {
               const uint16_t cp = code_pair(h);
               if (e % 4 == 0) codes[p][e / 4] = cp;
               else codes[p][e / 4] |= (uint32_t)cp << 16;
-              if (p + 1 < F::kParts) h = left16(h, cp);
+              if (p + 1 < F::kParts) h = left16(h, cp, p + 2 < F::kParts ? 0u : by_code);
             }
           }
           if (ok) {
