@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
       for (Walk wk(P, kWindow); ok && wk.more(); wk.next(P), ++seg) {
         for (int h = 0; ok && h <= wk.t.two; ++h) {
           uint64_t* bar = &ctl->q_full[qt & 1];
-          ok = wait_for(&ctl->q_empty[qt & 1], ((qt >> 1) & 1) ^ 1, ctl, P.wait_ns);
+          ok = wait_for<!kEight>(&ctl->q_empty[qt & 1], ((qt >> 1) & 1) ^ 1, ctl, P.wait_ns);
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           if (lane == 0) {
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
             const int page = of.of(c, wk.t, wk.blk + (b2 >> 1), lane);
             const int pages = __popc(__ballot_sync(kFullMask, page >= 0));
             const int st = kt % R::kStages8;
-            ok = wait_for(&ctl->empty8[st], ((kt / R::kStages8) & 1) ^ 1, ctl, P.wait_ns);
+            ok = wait_for<!kEight>(&ctl->empty8[st], ((kt / R::kStages8) & 1) ^ 1, ctl, P.wait_ns);
             ok = __all_sync(kFullMask, ok);
             if (!ok) break;
             if (lane == 0) {
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int st = kt % R::kStages;
-            ok = ok && wait_for(&ctl->empty[st], ((kt / R::kStages) & 1) ^ 1, ctl, P.wait_ns);
+            ok = ok && wait_for<!kEight>(&ctl->empty[st], ((kt / R::kStages) & 1) ^ 1, ctl, P.wait_ns);
             ok = __all_sync(kFullMask, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], (uint32_t)pages * c.page * D * 2);
@@ -774,8 +774,6 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
         ctl->asked = kt;
         ctl->asked_q = qt;
       }
-      if (blockIdx.x == 0 && (P.plan.start[0].w != 0) != kWindow)  // a plan of the other kind
-        for (int i = lane; i < P.n; i += 32) P.plan.status[i] = SAMSPEC_ST_BADPARAM;
     } else if (warp == 9) {
       // ---- matrix products ----
       if (lane == 0) {
@@ -792,10 +790,10 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
         int st = 0, par = 0;     // ring stage of the block's keys, its parity
         auto product = [&] {
           const int w = (g - 1) & 1;
-          ok = wait_for(&ctl->p_full[w], ((g - 1) >> 1) & 1, ctl, P.wait_ns);
-          if (v_what & kAwaitV) ok = ok && wait_for(&ctl->full[v_stage], (v_what & kParityV) != 0, ctl, P.wait_ns);
+          ok = wait_for<!kEight>(&ctl->p_full[w], ((g - 1) >> 1) & 1, ctl, P.wait_ns);
+          if (v_what & kAwaitV) ok = ok && wait_for<!kEight>(&ctl->full[v_stage], (v_what & kParityV) != 0, ctl, P.wait_ns);
           // the last segment's O has to be read before this one's begins
-          if (v_what & kAwaitO) ok = ok && wait_for(&ctl->o_free, (v_what & kParityO) != 0, ctl, P.wait_ns);
+          if (v_what & kAwaitO) ok = ok && wait_for<!kEight>(&ctl->o_free, (v_what & kParityO) != 0, ctl, P.wait_ns);
           if (!ok) return;
           tc_fence_after();
           const uint32_t vl = ring_low + v_stage * (R::kTile >> 4);
@@ -808,17 +806,17 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
           v_stage = -1;
         };
         for (int seg = 0, qt = 0; ok && !last; ++seg) {
-          ok = wait_for(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
+          ok = wait_for<!kEight>(&ctl->q_full[qt & 1], (qt >> 1) & 1, ctl, P.wait_ns);
           if (!ok) break;
           const int nb = ctl->seg[seg & 3].nb;
           const bool rows2 = ctl->seg[seg & 3].t.two;
           last = ctl->seg[seg & 3].last;
-          if (rows2) ok = wait_for(&ctl->q_full[(qt + 1) & 1], ((qt + 1) >> 1) & 1, ctl, P.wait_ns);
+          if (rows2) ok = wait_for<!kEight>(&ctl->q_full[(qt + 1) & 1], ((qt + 1) >> 1) & 1, ctl, P.wait_ns);
           const int items = rows2 ? 2 * nb : nb;
           for (int x = 0; ok && x < items; ++x, ++g) {
             const int w = g & 1, half = rows2 ? x & 1 : 0;
             const bool done = !rows2 || half == 1;  // with the block's keys
-            if (half == 0) ok = wait_for(&ctl->full[st], par, ctl, P.wait_ns);
+            if (half == 0) ok = wait_for<!kEight>(&ctl->full[st], par, ctl, P.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const uint32_t ql = q_low + ((qt + half) & 1) * (R::kTile >> 4), kl = ring_low + st * (R::kTile >> 4);
@@ -846,6 +844,9 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
       }
       __syncwarp();
     } else {
+      // (by the loader's warp, in its code: groups of 16 446 us instead of 442)
+      if (warp == 10 && blockIdx.x == 0 && (P.plan.start[0].w != 0) != kWindow)  // a plan of the other kind
+        for (int i = lane; i < P.n; i += 32) P.plan.status[i] = SAMSPEC_ST_BADPARAM;
       if constexpr (kEight) expand_tiles<T, D, kWindow>(P, smem, warp - 10, lane);
     }
   } else {
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
     // a segment has come: all threads of both streams decide alike whether to
     // go on, and are done with the last one's exchange and flag
     auto next_segment = [&](int q) {
-      const bool came = wait_for(&ctl->q_full[q & 1], (q >> 1) & 1, ctl, P.wait_ns);
+      const bool came = wait_for<!kEight>(&ctl->q_full[q & 1], (q >> 1) & 1, ctl, P.wait_ns);
       return !named_any(4, 256, !came);
     };
     if (!last) ok = next_segment(0);
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
       float m = -INFINITY, reach = -INFINITY, off = 0.f, l = 0.f;
       for (int x = x0; x < items; x += 2) {
         const bool edge = x >= x_edge || (kWindow && x < x_low);
-        if (ok) ok = wait_for(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
+        if (ok) ok = wait_for<!kEight>(&ctl->s_full[w], ((g0 + x) >> 1) & 1, ctl, P.wait_ns);
         ok = __all_sync(kFullMask, ok);
         tc_fence_after();
         if (ok && row == 0) {
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
         if (edge) {
           const int b = rows2 ? x >> 1 : x, k0 = block_key<kWindow>(sg.t, sg.blk + b);
           const int t_v = 2 * (kb + b) + 1, st = t_v % R::kStages;
-          if (ok) ok = wait_for(&ctl->full[st], (t_v / R::kStages) & 1, ctl, P.wait_ns);
+          if (ok) ok = wait_for<!kEight>(&ctl->full[st], (t_v / R::kStages) & 1, ctl, P.wait_ns);
           // (a unit of two row tiles: both streams use the values)
           if (ok)
             clean_values<T, D>(ring + st * R::kTile, kWindow && x < x_low ? 0 : max(sg.t.ctx - k0, 0),
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&ctl->p_full[w]);
       }
-      if (ok) ok = wait_for(&ctl->o_done, seg & 1, ctl, P.wait_ns);
+      if (ok) ok = wait_for<!kEight>(&ctl->o_done, seg & 1, ctl, P.wait_ns);
       // (the streams' maxima and sums); all threads decide alike whether to go on
       const bool both = !rows2 && items > 1;
       ctl->ml[w][row] = {m, l};
