@@ -58,9 +58,10 @@ extern "C" {
  * kv_append writes, with e the smallest number in -32 .. 7 for which no element of
  * the head exceeds 448 * 2^e, the byte e + 127 and each element times 2^-e, rounded
  * to the nearest code, ties to even: off by at most 2^-4 of the element, or 2^(e - 10)
- * if that is more; magnitudes beyond 57344 count as that.  Of a rotated element it is
- * the code of its exact value, where it is at least a third of its pair and
- * 2^(e - 6); of its fp32 value else.
+ * if that is more; magnitudes beyond 57344 count as that.  A rotated head's e is that of its
+ * fp32 values.  Of a rotated element it is the code of its exact value, where it is at
+ * least a third of its pair and 2^(e - 6), and not within position * 2^-62 of its pair of
+ * a tie between two codes; of its fp32 value else.
  * A head with an element that is not finite gets byte 255 and is NaN as a whole.
  * Of bytes written by others, those outside 95 .. 134 count as the nearest (but for
  * 255).  The two codes that e4m3 has for NaN are not written: kv_read takes those of
@@ -178,7 +179,8 @@ int kv_plan_window(const kv_cache* cache, const int32_t* d_rows, int32_t n, int3
 /* Puts the new tokens' keys and values into their slots of one layer and turns
  * queries and keys to their positions: pair j of the first `rot` elements of
  * a head is rotated by position * d_inv_freq[j] radians (fp64 [rot / 2]; the
- * angle is reduced exactly, whatever the position) and scaled by mscale.
+ * angle without its whole turns is exact to position * 2^-62, whatever the position, and then
+ * taken in fp32) and scaled by mscale.
  * layout: pairs (j, j + rot / 2) for SAMSPEC_ROPE_HALF, (2j, 2j + 1) for
  * SAMSPEC_ROPE_INTERLEAVED.  rot = 0: no rotation.  d_q [n, N, q_heads,
  * head_dim] -> d_q_out (contiguous; may be d_q; both may be NULL), d_k and

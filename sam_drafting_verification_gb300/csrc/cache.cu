@@ -418,6 +418,17 @@ __global__ void __launch_bounds__(256) set_len_kernel(KvView c, const int32_t* r
 }
 
 // ---- rotary append -----------------------------------------------------------
+// f / 2 pi in 64 bits of a turn, without whole ones, the nearest (for |f| < 2^53): f's 53
+// bits times the first 128 of 1 / 2 pi, in integers.  (With sums of two doubles, as exact,
+// a call took 1 us longer: the prologue of every CTA, at two of their operations a clock.)
+__device__ __forceinline__ uint64_t turn_of(double f) {
+  const uint64_t u = (uint64_t)__double_as_longlong(f);
+  const int ex = (int)(u >> 52) & 0x7ff, e = ex - 1075;  // f = +-m 2^e
+  const uint64_t m = (u & 0xfffffffffffffull) | (ex ? 1ull << 52 : 0);
+  const unsigned __int128 x = (unsigned __int128)m * 0x28be60db9391054aull + __umul64hi(m, 0x7f09d5f47d4d3770ull);
+  const uint64_t t = e < 0 ? (uint64_t)(((x >> (min(-e, 127) - 1)) + 1) >> 1) : e < 64 ? (uint64_t)x << e : 0;
+  return u >> 63 ? 0 - t : t;
+}
 struct AppendParams {
   KvView c;
   PlanView plan;
@@ -479,8 +490,8 @@ __device__ __forceinline__ uint32_t four_codes(float2 a, float2 b, float inv) {
 // Angles: pair j turns by position * f_j.  f_j / 2 pi, without its whole
 // turns, is held as a 64-bit fraction of a turn; the position times that, in
 // 64-bit arithmetic that wraps, is the angle with whole turns gone, exact to
-// position * 2^-53 turns whatever the position.  Its top bits go to fp32 half
-// turns in [-1, 1) for sincospif.
+// position * 2^-65 turns whatever the position (2^-31 radians for the farthest).  Its
+// top bits go to fp32 half turns in [-1, 1) for sincospif.
 //
 // A warp takes a token (for few tokens, a part of its heads): its sines and
 // cosines, then its heads, four 16-byte loads of a lane in flight, on three CTAs an SM
@@ -529,9 +540,7 @@ __global__ void __launch_bounds__(256, 3) append_kernel(AppendParams P) {
   wait_for_previous();
   let_next_start();
   for (int j = tid; j < half; j += 256) {
-    double f = P.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
-    f -= floor(f);
-    turn[j] = (uint64_t)(f * 18446744073709551616.0);
+    turn[j] = turn_of(P.inv_freq[j]);
     axis[j] = P.axis ? min(max(P.axis[j], 0), P.axes - 1) : 0;
   }
   __syncthreads();
