@@ -62,10 +62,11 @@ extern "C" {
  * fp32 values.  Of a rotated element it is the code of its exact value, where it is at
  * least a third of its pair and 2^(e - 6), and not within position * 2^-62 of its pair of
  * a tie between two codes; of its fp32 value else.
- * A head with an element that is not finite gets byte 255 and is NaN as a whole.
- * Of bytes written by others, those outside 95 .. 134 count as the nearest (but for
- * 255).  The two codes that e4m3 has for NaN are not written: kv_read takes those of
- * others for +-480, a token that sees one has no defined result.
+ * A head with an element that is not finite gets byte 255 and is NaN as a whole,
+ * whatever its codes (a NaN's is one of the two that e4m3 has for NaN).  Of bytes written
+ * by others, those outside 95 .. 134 count as the nearest (but for 255).  In a head with
+ * another byte those two codes are not written: kv_read takes others' for +-480, a
+ * token that sees one has no defined result.
  * The scales move with the codes wherever pages are copied or compacted.
  * Limits: page 16, 32, 64 or 128; head_dim 64 or 128; 1 <= kv_heads <= 1024;
  * 1 <= layers; seqs, max_pages <= 2^20; max_pages * page < 2^30; n_pages *

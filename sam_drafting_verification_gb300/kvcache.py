@@ -198,9 +198,9 @@ class KVCache:
         int32 [seqs], refs int32 [pages], free int32 [ceil(pages / 32)] (a bit
         for each page, set where refs is 0); of a cache of 8 bits k_scale and v_scale
         uint8 [layers, pages, kv_heads, page] and io_dtype (bytes outside 95 .. 134, but
-        for 255, count as the nearest; the codes 0x7f and 0xff, which append never
-        writes, read as +-480, and attend has no defined result for a token that sees
-        one)."""
+        for 255, count as the nearest; the codes 0x7f and 0xff, which append writes only
+        in heads of byte 255, read as +-480 in others, and attend has no defined result
+        for a token that sees one there)."""
         self = cls.__new__(cls)
         self._set(k, v, table, lens, held, refs, free, k_scale, v_scale, io_dtype)
         return self
