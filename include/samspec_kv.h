@@ -171,7 +171,9 @@ int kv_plan(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N, 
  * `sinks` of its sequence (>= 0).  A committed key's position is its slot.  The
  * rest is kv_plan's, the plan's size too (grouped: 0; what sequences share is read
  * by each of them).  kv_append takes either plan; this one's attention is
- * kv_attend_window.  Of a sequence's pages only those that its tokens see are read. */
+ * kv_attend_window.  Of a sequence's pages only those that its tokens see are read, but
+ * a window gives none back: a sequence holds all of its pages, those behind every window
+ * too (ST_PAGE where the table has none). */
 int kv_plan_window(const kv_cache* cache, const int32_t* d_rows, int32_t n, int32_t N,
                    int32_t q_heads, const int32_t* d_n_tok, const int32_t* d_first_child,
                    const int32_t* d_next_sibling, int32_t window, int32_t sinks, void* d_plan,
@@ -224,7 +226,10 @@ int kv_read(const kv_cache* cache, int32_t layer, const int32_t* d_rows, int32_t
  * (contiguous, 32-byte aligned, the cache's dtype, or io_dtype) = softmax(scale *
  * q k^T) v over the keys that each token sees (query head h reads key head h /
  * (q_heads / kv_heads)), scale positive and finite.
- * Scores, softmax and sums in fp32; the probabilities are rounded to the
+ * Scores, softmax and sums in fp32 (sums as the matrix unit adds them: it may cut a
+ * product at the last place of the sum so far, 2^-23 of it, always toward zero: half a
+ * million keys of which each has 2^-20 of one key's weight can lose 1% of theirs); the
+ * probabilities are rounded to the
  * cache's dtype (or io_dtype) for the product with v.  A cache of 8 bits with no
  * groups and N * q_heads / kv_heads <= 32: so are products of a probability and its
  * value's scale, but small ones to multiples of 2^-17 (F16: 2^-19) of the row's

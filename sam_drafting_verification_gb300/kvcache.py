@@ -371,7 +371,8 @@ class KVCache:
         sizes, written again in place.  window: layers whose tokens see the last
         `window` positions only, their own among them, and the first `sinks` of
         their sequence (group changes nothing there: each sequence reads what it
-        sees); a model with both kinds of layers makes two plans a pass."""
+        sees); a model with both kinds of layers makes two plans a pass.  A window
+        saves reads and no memory: sequences hold the pages behind it all the same."""
         N, q_heads = int(N), int(q_heads)
         if window is None:
             if sinks != 0:
