@@ -226,21 +226,20 @@ int kv_read(const kv_cache* cache, int32_t layer, const int32_t* d_rows, int32_t
  * (contiguous, 32-byte aligned, the cache's dtype, or io_dtype) = softmax(scale *
  * q k^T) v over the keys that each token sees (query head h reads key head h /
  * (q_heads / kv_heads)), scale positive and finite.
- * Scores, softmax and sums in fp32 (sums as the matrix unit adds them: it may cut a
- * product at the last place of the sum so far, 2^-23 of it, always toward zero: half a
- * million keys of which each has 2^-20 of one key's weight can lose 1% of theirs); the
- * probabilities are rounded to the
- * cache's dtype (or io_dtype) for the product with v.  A cache of 8 bits with no
- * groups and N * q_heads / kv_heads <= 32: so are products of a probability and its
- * value's scale, but small ones to multiples of 2^-17 (F16: 2^-19) of the row's
- * largest such product, or of 2^-21 (2^-23) where a key exceeds those about it by 2^8: up
- * or down, as a number says that runs evenly through such a step from key to key,
- * so with a mean of zero: n keys' errors add up to about sqrt(n) of one.  An element of a
- * query is off by up to 2^-21 (2^-25) of the largest of its head; a query with an
- * element that is not finite gets NaN.
- * Keys and values outside a token's
- * sight never reach it, whatever they hold (infinities and NaN included).  A
- * query all of whose scores are -infinity gets zeros.
+ * Scores, softmax and sums in fp32 (sums as the matrix unit adds them: it cuts products,
+ * toward zero, below the last places of the sum so far; of a million keys with 2^-23.5 of
+ * one key's weight each, 8% of all, 1.2% of all were lost); the probabilities are rounded
+ * to the cache's dtype (or io_dtype) for the product with v.
+ * A cache of 8 bits with no groups and N * q_heads / kv_heads <= 32: products of a
+ * probability and its value's scale are rounded so, but small ones to multiples of 2^-17
+ * (F16: 2^-19) of the row's largest such product, or of 2^-21 (2^-23) where a key exceeds
+ * those about it by 2^8: up or down, as a number says that runs evenly through such a
+ * step from key to key, so with a mean of zero: n keys' errors add up to about sqrt(n)
+ * of one.  (Little is cut there: of those keys' 1.2%, nothing.)  An element of a query is
+ * off by up to 2^-21 (2^-25) of the largest of its head; a query with an element that
+ * is not finite gets NaN.
+ * Keys and values outside a token's sight never reach it, whatever they hold
+ * (infinities and NaN included).  A query all of whose scores are -infinity gets zeros.
  * Tokens beyond n_tok, or of a sequence with a status, get zeros. */
 int kv_attend(const kv_cache* cache, int32_t layer, void* d_plan, size_t plan_bytes, int32_t n,
               int32_t N, int32_t q_heads, const void* d_q, int64_t q_stride, float scale,

@@ -528,10 +528,11 @@ __device__ __forceinline__ void add_unclean(const AttendParams& P, int seq_row, 
 }
 
 // The warps that turn tiles of codes into tiles of 16 bits, in the order of the copies:
-// six of them (64 sequences of 4096 keys, 64 rows: 230 us, with five 243, four 254, three
-// 306), in one place of the code (in two, 310: it is read through a cache).  A warp takes
-// 32 of the 16-byte pieces of codes at a time, each 2 pieces of a row (2 pc, 2 pc + 1),
-// reading the next 32 meanwhile (212 us; all of them beforehand 219); the upper half of a
+// six of them (64 sequences of 4096 keys, 64 rows, us a call: 230 when that was chosen, with
+// five 243, four 254, three 306), in one place of the code (in two, 310: it is read through
+// a cache).  A warp takes 32 of the 16-byte pieces of codes at a time, each 2 pieces of a
+// row (2 pc, 2 pc + 1), reading the next 32 meanwhile (230 -> 212, all of them beforehand
+// 219; now 205, L2 flushed before the call); the upper half of a
 // 128-wide row's lanes writes the odd one first, so that eight lanes meet eight groups of
 // banks.  A lane makes the factor of one of the warp's rows, the lanes of a row take it
 // from there.
@@ -626,8 +627,8 @@ __device__ __forceinline__ void expand_tiles(const AttendParams& P, unsigned cha
 // 442 -> 452 us, prompt chunks 122 -> 126), and both bodies in one kernel spill.
 //
 // What bounds a window: units' starts and ends.  64 sequences, trees' or chains' 4
-// tokens, windows of 1024 keys, 8 heads of 128: 64 us, 4.6 TB/s, for units of 9 to 10
-// blocks; 4 chunks of 1000 tokens in windows of 512: 59 us for units of 5 to 7.
+// tokens, windows of 1024 keys, 8 heads of 128: 66 us for this kernel, 4.6 TB/s, for units
+// of 9 to 10 blocks; 4 chunks of 1000 tokens in windows of 512: 59 us for units of 5 to 7.
 //
 // kEight: of a cache of 8 bits, for what attend_few_kernel does not take.  TMA brings
 // codes and scales as they lie in their pages; warps 10 to 15 turn each tile into 16
@@ -635,9 +636,11 @@ __device__ __forceinline__ void expand_tiles(const AttendParams& P, unsigned cha
 // follows is the same, and results are those of a 16-bit cache that holds the codes'
 // values.  A block is 128 keys * (D + 1) * 2 bytes, 1400 clocks of an SM's share of
 // HBM.  What bounds it: the six warps for one tile of rows, as they take 3600 clocks for
-// a block; the softmax's chain, which they share the issue slots with, for two (4 chunks
-// of 1000 tokens behind 0 to 4000 keys, 32 heads on 8 of 128: a call takes 137 us, over
-// a cache of 16 bits 123).
+// a block; the softmax's chain, which they share the issue slots with, for two.  So it
+// saves memory, not time: 64 sequences of 4096 keys, 8 heads of 128 (64), 64 rows, 205 (150)
+// us a call, L2 flushed before it, over a cache of 16 bits 190 (127); groups of 8 with
+// 4096 keys shared 103 and 93; 4 chunks of 1000 tokens behind 0 to 4000 keys, 32 heads
+// on 8 of 128, 136 and 122.
 template <typename T, int D, bool kWindow, bool kEight>
 __global__ void __launch_bounds__(Ring<D, kEight>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap map_k,

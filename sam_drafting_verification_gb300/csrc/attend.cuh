@@ -202,9 +202,9 @@ struct Segment {  // what the loader hands on of a segment
 // exceeds the limit raises the flag for all.  Flag and clock (in units of 1024 ns)
 // are read only every 1024 tries, and the loop is kept small: a kernel has a dozen
 // of them between the code of its roles, which is read through a cache (unrolled, with
-// the clock in 64 bits: 64-wide heads over 16k-32k 8-bit keys 188 us instead of 158).
-// kAhead: a try before the loop, which the kernel for 16 bits is better off with (64-wide
-// heads over 16k-32k keys 160 us instead of 163).
+// the clock in 64 bits, 64-wide heads over 16k-32k 8-bit keys took 188 us a call instead of
+// 158).  kAhead: a try before the loop, which the kernel for 16 bits is better off with
+// (64-wide heads over 16k-32k keys 160 us instead of 163).
 template <bool kAhead = false, typename C>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, C* ctl, uint64_t limit) {
   if (kAhead && mbar_try_wait(bar, parity)) return true;

@@ -28,18 +28,18 @@ namespace {
 // weight goes up as often as it has parts of a step, and errors of n keys add up like
 // sqrt(n) of them, without a direction.
 //
-// A thread has a key: the key's two scales are its own, its scores are R numbers.
-// Weights are 2^(s + c) for a row's reference c, moved only when a weight would pass
-// 2^8.5: then (all rows for the first block, later single ones) the warpgroup takes
-// those rows' maxima, and what is there is scaled.  Where they are put: high, and small
-// weights have more steps left; low, and fewer maxima to come move the reference (2500
-// clocks: 64 sequences of 4096 keys, 32 rows of random queries: always at 2^8 222 us a call,
-// at 2^6 169, at 2^4 150; fp16 over 16k to 32k keys 232 at 2^8, 197 at 2^6, 159 at 2^4,
-// 140 at 2^2).  A row whose four warps' maxima lie together has many keys to share its
-// weight, and can have it low; where they lie apart one key may have all of it, few are
-// still to exceed it, and it goes high.  Else a step needs one vote of 128
-// threads.  The values' scale multiplies the weights on their way to the product, not
-// those of the sum.
+// A thread has a key: the key's two scales are its own, its scores are R numbers.  Weights
+// are 2^(s + c) for a row's reference c, moved only when a weight would pass 2^8.5: then
+// (all rows for the first block, later single ones) the warpgroup takes those rows'
+// maxima, and what is there is scaled.  Where they are put: high, and small weights have
+// more steps left; low, and fewer maxima to come move the reference (2500 clocks; a call,
+// L2 flushed before it, over 64 sequences of 4096 keys with 32 rows of random queries:
+// always at 2^8 222 us, at 2^6 169, at 2^4 150; fp16, 32 sequences of 16k to 32k keys,
+// 232 at 2^8, 197 at 2^6, 159 at 2^4, 140 at 2^2).  A row whose four warps' maxima lie
+// together has many keys to share its weight, and can have it low; where they lie apart
+// one key may have all of it, few are still to exceed it, and it goes high.  Else a step
+// needs one vote of 128 threads.  The values' scale multiplies the weights on their way
+// to the product, not those of the sum.
 //
 // Two streams of steps, blocks in turn, as in attend_kernel; warps 8 and 12 load keys
 // with the scales, and values (one warp for both, or the scales with a warp of their
@@ -49,12 +49,12 @@ namespace {
 // far ahead, into the next unit too: a stream's chain is its softmax alone.
 //
 // What bounds it.  A block is 128 keys * (D + 1) * 2 bytes: at D 128 1400 clocks of an
-// SM's share of HBM.  64 sequences of 4096 keys, 8 heads of 128, 16 rows: 100 us, 5.4
-// TB/s of 6.8; the rest are units' starts and ends.  At D 64 a block comes in 700
-// clocks, and fp16 has three parts to make: 32 sequences of 16k to 32k keys, 4 heads of
-// 64, 32 rows: 121 us, 3.4 TB/s.  There the softmax bounds it, of 128 * 32 weights a
-// block at 10 instructions each: half of the issue slots are taken, and a warp that
-// could issue waits for its instructions as often as not (the loops' code is 30 KB).
+// SM's share of HBM.  64 sequences of 4096 keys, 8 heads of 128, 16 rows: 100 us for this
+// kernel, 5.4 TB/s of 6.8; the rest are units' starts and ends.  At D 64 a block comes in
+// 700 clocks, and fp16 has three parts to make: 32 sequences of 16k to 32k keys, 4 heads
+// of 64, 32 rows: 124 us for it, 3.2 TB/s.  There the softmax bounds it, of 128 * 32
+// weights a block at 10 instructions each: half of the issue slots are taken, and a warp
+// that could issue waits for its instructions as often as not (the loops' code is 30 KB).
 constexpr float kReach = 8.5f;  // log2 of the largest weight (e4m3 has 448)
 constexpr float kEven = 4.f;    // how far apart (log2) maxima of 32 keys may lie for a reference put low
 constexpr int kMaxStages = 12;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(512, 1)
       const int x_edge = before > 0 ? before / kKeyBlock : 0;
       const int x_low = kWindow && sg.t.low > 0 ? (sg.t.low - sg.t.kbeg + kKeyBlock - 1) / kKeyBlock - first : 0;
       // sums; up to 16 rows' scales and references are held, more are read in each step (held for
-      // 32, 64-wide heads over 16k-32k keys take 191 us, and 175 read)
+      // 32, 64-wide heads over 16k-32k keys took 191 us a call where they took 175 read)
       constexpr int kHeld = R <= 16 ? R : 1;
       float l[R], sr[kHeld], cr[kHeld];
       uint32_t unset = first_bits(rows);  // rows without a reference

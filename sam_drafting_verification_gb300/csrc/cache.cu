@@ -493,32 +493,33 @@ __device__ __forceinline__ uint32_t four_codes(float2 a, float2 b, float inv) {
 // position * 2^-65 turns whatever the position (2^-31 radians for the farthest).  Its
 // top bits go to fp32 half turns in [-1, 1) for sincospif.
 //
-// A warp takes a token (for few tokens, a part of its heads): its sines and
-// cosines, then its heads, four 16-byte loads of a lane in flight, on three CTAs an SM
-// (a call for the prompts below 54 and 132 us; two CTAs with eight loads 58 and 137;
-// three with five or six, which spill more, 58 to 66 and 134; four with three 56 and
-// 138).  A lane's place in a head is the same for all of them, and so are its sines and
-// cosines; in the half layout the other elements of its pairs come from the lane that
-// has loaded them.  With positions given, pair j's is that of its axis: one more read, of
-// neighbours in a line, beside those of the table.  Reads q, k, v and writes q', K, V
-// once: bound by HBM for prompts, by latency for a decode step.
-// (8 prompts of 1250 to 2500 tokens, 16 and 4 heads of 128, three axes: 43 us, 3.2
+// A warp takes a token (for few tokens, a part of its heads): its sines and cosines, then
+// its heads, four 16-byte loads of a lane in flight, on three CTAs an SM (a call for the
+// prompts below, L2 flushed before it, 54 and 132 us when that was chosen, 54 and 138
+// now; two CTAs with eight loads 58 and 137; three with five or six, which spill more, 58
+// to 66 and 134; four with three 56 and 138).  A lane's place in a head is the same for
+// all of them, and so are its sines and cosines; in the half layout the other elements of
+// its pairs come from the lane that has loaded them.  With positions given, pair j's is
+// that of its axis: one more read, of neighbours in a line, beside those of the table.
+// Reads q, k, v and writes q', K, V once: bound by HBM for prompts, by latency for a
+// decode step.
+// (8 prompts of 1250 to 2500 tokens, 16 and 4 heads of 128, three axes: 41 us, 3.2
 // TB/s: a token is a chain of reads, its page, position, heads, and a warp has six.)
 //
 // kEight: into a cache of 8 bits.  The lanes that hold a head take its largest
 // magnitude together (4 exchanges), from the values that rotation gives: one rounding
 // between a key and its code.  (8 prompts of up to 4001 tokens, 32 and 8 heads
-// of 128: 89 us for 473 MB, 5.3 TB/s, a quarter of it zeros for the queries of tokens
+// of 128: 93 us for 473 MB, 5.1 TB/s, a quarter of it zeros for the queries of tokens
 // that take no part.)
 //
 // A code keeps four bits of an element, so where fp32 leaves it beside a tie, the last
 // bits of the angle, of sincospif and of two roundings decide the code.  Within 16 of its
 // last places of one (one element in 2^15; the fp32 value is off by less than 16 / 3 *
 // 2^-24 of its pair: angle 1.6, cosine and sine 1.4, roundings 2) its head is done again,
-// such elements in 64 bits, handed over rounded to odd (cut, with the last bit set for what
-// is cut off), so that the code is rounded once.  (8 prompts: 132 -> 136 us a call, and keys
-// off from exact ones by 1e-6 instead of 5e-5; inside the loop over vectors, with their
-// registers held, 144.)
+// such elements in 64 bits, handed over rounded to odd (cut, with the last bit set for
+// what is cut off), so that the code is rounded once.  (8 prompts, L2 flushed before the
+// call: 132 -> 136 us, and keys off from exact ones by 1e-6 instead of 5e-5; inside the
+// loop over vectors, with their registers held, 144.)
 __device__ __forceinline__ bool near_tie(float f) { return (__float_as_uint(f) & 0xfffffu) - 0x7fff0u <= 32u; }
 // Is f exact, as the pair is not turned (g: cosine and sine times m)?  At a position of 0
 // an element is the 16-bit input, of which one in 16 (bf16) is a tie.  (8 images of 50 x 50

@@ -208,9 +208,11 @@ struct KvJoin {
 };
 inline __host__ __device__ int tile_tokens(int rep) { return kRows / rep; }
 // Do a pass's units have few enough rows for attend_few_kernel?  Its time goes by the
-// rows, attend_kernel's does not up to 128.  64 sequences of 4096 8-bit keys and 8 key
-// heads, us a call: 16 rows 128 (128 elements a head) and 97 (64), 32 rows 173 and 138-146, by
-// attend_kernel 212 and 156; 64 rows took 351 and 309.
+// rows, attend_kernel's hardly up to 128.  64 sequences of 4096 8-bit keys and 8 key heads of
+// 128 (64) elements, us a call, L2 flushed before it: 16 rows 119 (90), by attend_kernel 197
+// (145); 32 rows 150 (122), by attend_kernel 199 (147); 64 rows, by attend_kernel, 205
+// (150), where an earlier attend_few_kernel took 351 (309).  In windows of 1024 keys 32 rows
+// take 119, by attend_kernel 111, but 16 take 78 and 107.
 inline bool few_rows(const KvView& c, int N, int rep, bool grouped) {
   return c.elt == 1 && !grouped && (int64_t)N * rep <= 32;
 }

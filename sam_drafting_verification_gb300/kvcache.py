@@ -162,7 +162,9 @@ class KVCache:
     pages held, references and free pages.  The tensors are the caller's to
     read; only the calls below change them.
 
-    dtype torch.float8_e4m3fn: a cache of 8 bits, half the size.  append quantises
+    dtype torch.float8_e4m3fn: a cache of 8 bits, half the size (attention over it is faster
+    than over 16 bits for up to 32 new tokens times query heads of a key head, without
+    groups and windows; else it takes as long or somewhat longer).  append quantises
     keys and values as it writes them, attend and read take them back; queries,
     new keys and values, and results are of io_dtype (bfloat16 or float16).  k_scale
     and v_scale uint8 [layers, pages, kv_heads, page] hold a byte b for each token and
